@@ -465,6 +465,187 @@ m2_status m2_state_update_host(m2_host_stage* stage, const m2_cache* cache, cons
  * step's copy in then also waits for `stream`'s work issued before it. */
 m2_status m2_host_stage_join(m2_host_stage* stage, m2_stream stream);
 
+/*
+ * The 8-bit state cache: the SSM state of a mixer layer as signed 8-bit codes
+ * with one fp32 scale per row of N values (a row is one (h, p)); the conv rows
+ * as in m2_cache. A state takes N + 4 bytes a row where bf16 takes 2N. No
+ * source that the library follows describes one; it keeps the slot, padding
+ * and error conventions of m2_cache.
+ *   a = max |v| over the row, both quotients rounded to fp32, then
+ *   scale = a / 127,  code = round half to even (v * (127 / a)),
+ * and a value reads back as code * scale, at most scale / 2 (and fp32
+ * rounding) from v. A row with a < 2^-100 is stored as zeros. A row that holds
+ * an infinity or a NaN reads back as NaN in every value: its scale is NaN.
+ * Every store rounds: a state that stays parked is rounded once, one that
+ * decodes on the 8-bit cache once a token.
+ */
+typedef struct m2_q8_cache {
+    int8_t* ssm;      /* [num_slots, H, P, N] codes, N fastest */
+    float* scale;     /* [num_slots, H, P] */
+    void* conv;       /* [num_slots, K-1, conv_dim] act_dtype */
+    int32_t* error;   /* device int32 error word, or NULL */
+    int64_t num_slots;
+    m2_shape shape;   /* state_dtype is not used */
+    int32_t device;   /* CUDA device ordinal of the buffers */
+} m2_q8_cache;
+
+/* M2_OK when the 8-bit kernels implement `shape` (N 64, 128 or 256, P a
+ * multiple of 8 up to 256, and at most 8192 rows a group, 4096 at N = 256);
+ * otherwise as m2_shape_check. Host only, no CUDA. */
+m2_status m2_q8_shape_check(const m2_shape* shape);
+
+/* Bytes of the codes, the scales and the conv rows of num_slots slots. Host
+ * only, no CUDA. Each output may be NULL. */
+m2_status m2_q8_cache_bytes(const m2_shape* shape, int64_t num_slots, int64_t* code_bytes,
+                            int64_t* scale_bytes, int64_t* conv_bytes);
+
+/* Describes caller-owned buffers as an 8-bit cache; ssm, scale and conv must
+ * be 16-byte aligned, error_word may be NULL. The calls below must be made
+ * with the device current on which it was described (M2_ERR_INVALID_ARG
+ * otherwise). Nothing is allocated or launched. Slots whose codes are zero
+ * hold zero states whatever their scale, as long as it is finite. */
+m2_status m2_q8_cache_wrap(const m2_shape* shape, int64_t num_slots, int8_t* ssm, float* scale, void* conv,
+                           int32_t* error_word, m2_q8_cache* out);
+
+/* Zeroes the states and the conv rows of n slots, as m2_cache_zero_slots. Two
+ * launches. */
+m2_status m2_q8_zero_slots(const m2_q8_cache* cache, int32_t n, const int32_t* slot_idx, m2_stream stream);
+
+/*
+ * Copies n sequences from a 16- or 32-bit cache into an 8-bit one, quantising
+ * the states as they are written: dst slot dst_idx[i] takes the state and the
+ * conv rows of src slot src_idx[i] (device int32 arrays). src and dst have the
+ * same H, P, N, G, K and act_dtype (M2_ERR_INVALID_ARG otherwise). A pair with
+ * a negative index is skipped; an index past its cache's slots records
+ * M2_ERR_BAD_SLOT in that cache's error word and skips the pair. src_idx may
+ * repeat a slot; the non-negative dst_idx must be distinct. One launch.
+ */
+m2_status m2_q8_store(const m2_cache* src, const m2_q8_cache* dst, int32_t n, const int32_t* src_idx,
+                      const int32_t* dst_idx, m2_stream stream);
+
+/* The reverse: dst slot dst_idx[i] takes the values that src slot src_idx[i]
+ * stands for, rounded to dst's state dtype. src_idx may repeat a slot (one
+ * snapshot starts several sequences). Otherwise as m2_q8_store. One launch. */
+m2_status m2_q8_load(const m2_q8_cache* src, const m2_cache* dst, int32_t n, const int32_t* src_idx,
+                     const int32_t* dst_idx, m2_stream stream);
+
+/*
+ * m2_state_update with the conv fused, in place on an 8-bit cache: the state
+ * is read as code * scale, updated in fp32, y taken from the unrounded new
+ * state, and the new state stored as codes and scales in the same launch. The
+ * arguments are those of m2_state_update with conv non-NULL (conv must be
+ * given; xBC is the raw row in act_dtype). At most 65535 rows. One launch, no
+ * scratch memory.
+ */
+m2_status m2_q8_state_update(const m2_q8_cache* cache, const m2_ssm_params* ssm, const m2_conv_params* conv,
+                             int32_t batch, const void* xBC, int64_t xBC_row_stride, const void* dt,
+                             int64_t dt_row_stride, const void* z, int64_t z_row_stride, void* y,
+                             int64_t y_row_stride, const int32_t* slot_idx, m2_stream stream);
+
+/* m2_q8_state_update with the gated RMSNorm of m2_state_update_norm fused. */
+m2_status m2_q8_state_update_norm(const m2_q8_cache* cache, const m2_ssm_params* ssm,
+                                  const m2_conv_params* conv, const m2_norm_params* norm, int32_t batch,
+                                  const void* xBC, int64_t xBC_row_stride, const void* dt,
+                                  int64_t dt_row_stride, const void* z, int64_t z_row_stride, void* y,
+                                  int64_t y_row_stride, const int32_t* slot_idx, m2_stream stream);
+
+/* m2_get_device_error of an 8-bit cache. */
+m2_status m2_q8_get_device_error(const m2_q8_cache* cache, m2_stream stream, int32_t* out_code);
+
+/*
+ * The selective scan with a decay per channel and state (the mixer whose
+ * kernels a trace names conv1d and selective_scan_fwd, "Hybrid
+ * Mamba-Transformer MoEs hide their stalls in places dashboards do not look"):
+ * D channels of N states, B and C shared by the D/G channels of a group
+ * g(d) = d / (D/G):
+ *     dt = softplus(dt_raw[d] + dt_bias[d]);  A = -exp(A_log[d,n])
+ *     h[d,n] <- h[d,n]*exp(dt*A) + (dt*x[d])*B[g,n]
+ *     y[d]    = sum_n h[d,n]*C[g,n] + D[d]*x[d],  times silu(z[d]) if z
+ * Its conv covers the D channels of x only; B, C and dt are projected from the
+ * conv's output by the caller, so the conv is a call of its own.
+ */
+typedef struct m2_sel_shape {
+    int32_t channels;    /* D */
+    int32_t d_state;     /* N: 8, 16, 32, 64 or 128 */
+    int32_t ngroups;     /* G, divides D; D/G channels must fill 16-byte vectors */
+    int32_t d_conv;      /* K, conv width (2..8) */
+    int32_t state_dtype; /* M2_F32 or M2_BF16 */
+    int32_t act_dtype;   /* of x, dt_raw, B, C, z, y and the conv (M2_F32 or M2_BF16) */
+} m2_sel_shape;
+
+typedef struct m2_sel_cache {
+    void* ssm;         /* [num_slots, D, N] state_dtype, N fastest */
+    void* conv;        /* [num_slots, K-1, D] act_dtype: the last K-1 raw inputs, oldest row first */
+    int32_t* error;    /* device int32 error word, or NULL */
+    int64_t num_slots;
+    m2_sel_shape shape;
+    int32_t device;    /* CUDA device ordinal of the buffers */
+} m2_sel_cache;
+
+/* fp32 parameters: A_log [D, N], dt_bias [D], D [D] (device pointers, A_log
+ * 16-byte aligned). */
+typedef struct m2_sel_params {
+    const float* A_log;
+    const float* dt_bias;
+    const float* D;
+} m2_sel_params;
+
+/* As m2_shape_check, m2_cache_bytes and m2_cache_wrap; host only. The calls
+ * below must be made with the device current on which the cache was described. */
+m2_status m2_sel_shape_check(const m2_sel_shape* shape);
+m2_status m2_sel_cache_bytes(const m2_sel_shape* shape, int64_t num_slots, int64_t* ssm_bytes,
+                             int64_t* conv_bytes);
+m2_status m2_sel_cache_wrap(const m2_sel_shape* shape, int64_t num_slots, void* ssm, void* conv,
+                            int32_t* error_word, m2_sel_cache* out);
+
+/* As m2_cache_zero_slots. */
+m2_status m2_sel_zero_slots(const m2_sel_cache* cache, int32_t n, const int32_t* slot_idx, m2_stream stream);
+
+/* m2_conv1d_update and m2_conv1d_update_varlen over the D channels of x:
+ * weight [D, K], bias [D] or NULL. */
+m2_status m2_sel_conv1d_update(const m2_sel_cache* cache, const m2_conv_params* conv, int32_t batch,
+                               int32_t seqlen, const void* x, int64_t x_row_stride, void* x_out,
+                               int32_t out_dtype, int64_t out_row_stride, const int32_t* slot_idx,
+                               m2_stream stream);
+m2_status m2_sel_conv1d_update_varlen(const m2_sel_cache* cache, const m2_conv_params* conv, int32_t nseq,
+                                      const int32_t* cu_seqlens, int64_t total_tokens, int32_t max_seqlen,
+                                      const void* x, int64_t x_row_stride, void* x_out, int32_t out_dtype,
+                                      int64_t out_row_stride, const int32_t* slot_idx, m2_stream stream);
+
+/*
+ * One token per row, in place on cache->ssm at slot_idx[b].
+ *   x, dt, z, y  [batch, D] act_dtype, x post-conv, z may be NULL
+ *   B, C         [batch, G, N] act_dtype (a row's G*N values contiguous)
+ * The state is computed in fp32 and stored once; y is computed from the
+ * unrounded new state. Padding rows and bad slots as for m2_state_update. At
+ * most 65535 rows. One launch, no scratch memory.
+ */
+m2_status m2_sel_state_update(const m2_sel_cache* cache, const m2_sel_params* params, int32_t batch,
+                              const void* x, int64_t x_row_stride, const void* dt, int64_t dt_row_stride,
+                              const void* B, int64_t B_row_stride, const void* C, int64_t C_row_stride,
+                              const void* z, int64_t z_row_stride, void* y, int64_t y_row_stride,
+                              const int32_t* slot_idx, m2_stream stream);
+
+/*
+ * nseq prompts packed back to back, as for m2_chunk_scan_varlen: sequence b is
+ * rows cu_seqlens[b] .. cu_seqlens[b+1]-1, starts from cache->ssm[slot_idx[b]]
+ * (from zero when has_initial_state is NULL or has_initial_state[b] == 0) and
+ * leaves its final state there, rounded once. An empty sequence leaves its
+ * slot untouched; rows of y past the last sequence are not written.
+ * max_seqlen is a host bound on the lengths that only chooses how channels are
+ * spread over the GPU. The sums run in the order of the tokens in fp32. At most
+ * 65535 sequences. One launch, no scratch memory.
+ */
+m2_status m2_sel_scan(const m2_sel_cache* cache, const m2_sel_params* params, int32_t nseq,
+                      const int32_t* cu_seqlens, int64_t total_tokens, int32_t max_seqlen, const void* x,
+                      int64_t x_row_stride, const void* dt, int64_t dt_row_stride, const void* B,
+                      int64_t B_row_stride, const void* C, int64_t C_row_stride, const void* z,
+                      int64_t z_row_stride, void* y, int64_t y_row_stride, const int32_t* slot_idx,
+                      const uint8_t* has_initial_state, m2_stream stream);
+
+/* m2_get_device_error of a per-channel cache. */
+m2_status m2_sel_get_device_error(const m2_sel_cache* cache, m2_stream stream, int32_t* out_code);
+
 /* Debug/test path: synchronises `stream`, copies the cache's error word to
  * *out_code (0 or an m2_status value) and clears it. Not for hot loops. */
 m2_status m2_get_device_error(const m2_cache* cache, m2_stream stream, int32_t* out_code);

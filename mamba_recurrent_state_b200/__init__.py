@@ -16,10 +16,16 @@ record):
 * ``chunk_scan``    -- prefill scan landing on the same state as sequential
   updates.
 * ``Cache``         -- the fixed-size, slot-indexed state cache.
+* ``Q8Cache``, ``q8_store``, ``q8_load``, ``q8_state_update`` -- the state cache
+  in 8 bits: parked states and prefix snapshots, and the decode step on it.
+* ``SelCache``, ``sel_scan``, ``sel_state_update``, ``sel_conv1d_update`` -- the
+  selective scan with a decay per channel and state, for prompts and for
+  single tokens, with its causal conv.
 """
 
 from __future__ import annotations
 
+import contextlib
 import ctypes
 import dataclasses
 import os
@@ -86,6 +92,26 @@ class m2_norm_params(ctypes.Structure):
     _fields_ = [("weight", ctypes.c_void_p), ("eps", ctypes.c_float)]
 
 
+class m2_q8_cache(ctypes.Structure):
+    _fields_ = [("ssm", ctypes.c_void_p), ("scale", ctypes.c_void_p), ("conv", ctypes.c_void_p),
+                ("error", ctypes.c_void_p), ("num_slots", ctypes.c_int64), ("shape", m2_shape),
+                ("device", ctypes.c_int32)]
+
+
+class m2_sel_shape(ctypes.Structure):
+    _fields_ = [("channels", ctypes.c_int32), ("d_state", ctypes.c_int32), ("ngroups", ctypes.c_int32),
+                ("d_conv", ctypes.c_int32), ("state_dtype", ctypes.c_int32), ("act_dtype", ctypes.c_int32)]
+
+
+class m2_sel_cache(ctypes.Structure):
+    _fields_ = [("ssm", ctypes.c_void_p), ("conv", ctypes.c_void_p), ("error", ctypes.c_void_p),
+                ("num_slots", ctypes.c_int64), ("shape", m2_sel_shape), ("device", ctypes.c_int32)]
+
+
+class m2_sel_params(ctypes.Structure):
+    _fields_ = [("A_log", ctypes.c_void_p), ("dt_bias", ctypes.c_void_p), ("D", ctypes.c_void_p)]
+
+
 class m2_decode_rows(ctypes.Structure):
     _fields_ = [("batch", ctypes.c_int32), ("xBC", ctypes.c_void_p), ("xBC_row_stride", ctypes.c_int64),
                 ("dt", ctypes.c_void_p), ("dt_row_stride", ctypes.c_int64), ("z", ctypes.c_void_p),
@@ -147,6 +173,33 @@ SIGNATURES = {
                                     ctypes.POINTER(m2_conv_params), _I32, _P, _I64, _I64, _I64, _I64, _I64,
                                     _I64, _P, _I64, _P, _P]),
     "m2_host_stage_join": (_I32, [_P, _P]),
+    "m2_q8_shape_check": (_I32, [ctypes.POINTER(m2_shape)]),
+    "m2_q8_cache_bytes": (_I32, [ctypes.POINTER(m2_shape), _I64, ctypes.POINTER(_I64), ctypes.POINTER(_I64),
+                                 ctypes.POINTER(_I64)]),
+    "m2_q8_cache_wrap": (_I32, [ctypes.POINTER(m2_shape), _I64, _P, _P, _P, _P, ctypes.POINTER(m2_q8_cache)]),
+    "m2_q8_zero_slots": (_I32, [ctypes.POINTER(m2_q8_cache), _I32, _P, _P]),
+    "m2_q8_store": (_I32, [ctypes.POINTER(m2_cache), ctypes.POINTER(m2_q8_cache), _I32, _P, _P, _P]),
+    "m2_q8_load": (_I32, [ctypes.POINTER(m2_q8_cache), ctypes.POINTER(m2_cache), _I32, _P, _P, _P]),
+    "m2_q8_state_update": (_I32, [ctypes.POINTER(m2_q8_cache), ctypes.POINTER(m2_ssm_params),
+                                  ctypes.POINTER(m2_conv_params), _I32, _P, _I64, _P, _I64, _P, _I64, _P, _I64,
+                                  _P, _P]),
+    "m2_q8_state_update_norm": (_I32, [ctypes.POINTER(m2_q8_cache), ctypes.POINTER(m2_ssm_params),
+                                       ctypes.POINTER(m2_conv_params), ctypes.POINTER(m2_norm_params), _I32,
+                                       _P, _I64, _P, _I64, _P, _I64, _P, _I64, _P, _P]),
+    "m2_q8_get_device_error": (_I32, [ctypes.POINTER(m2_q8_cache), _P, ctypes.POINTER(_I32)]),
+    "m2_sel_shape_check": (_I32, [ctypes.POINTER(m2_sel_shape)]),
+    "m2_sel_cache_bytes": (_I32, [ctypes.POINTER(m2_sel_shape), _I64, ctypes.POINTER(_I64), ctypes.POINTER(_I64)]),
+    "m2_sel_cache_wrap": (_I32, [ctypes.POINTER(m2_sel_shape), _I64, _P, _P, _P, ctypes.POINTER(m2_sel_cache)]),
+    "m2_sel_zero_slots": (_I32, [ctypes.POINTER(m2_sel_cache), _I32, _P, _P]),
+    "m2_sel_conv1d_update": (_I32, [ctypes.POINTER(m2_sel_cache), ctypes.POINTER(m2_conv_params), _I32, _I32, _P,
+                                    _I64, _P, _I32, _I64, _P, _P]),
+    "m2_sel_conv1d_update_varlen": (_I32, [ctypes.POINTER(m2_sel_cache), ctypes.POINTER(m2_conv_params), _I32, _P,
+                                           _I64, _I32, _P, _I64, _P, _I32, _I64, _P, _P]),
+    "m2_sel_state_update": (_I32, [ctypes.POINTER(m2_sel_cache), ctypes.POINTER(m2_sel_params), _I32]
+                            + [_P, _I64] * 6 + [_P, _P]),
+    "m2_sel_scan": (_I32, [ctypes.POINTER(m2_sel_cache), ctypes.POINTER(m2_sel_params), _I32, _P, _I64, _I32]
+                    + [_P, _I64] * 6 + [_P, _P, _P]),
+    "m2_sel_get_device_error": (_I32, [ctypes.POINTER(m2_sel_cache), _P, ctypes.POINTER(_I32)]),
     "m2_get_device_error": (_I32, [ctypes.POINTER(m2_cache), _P, ctypes.POINTER(_I32)]),
     "m2_status_string": (ctypes.c_char_p, [_I32]),
     "m2_version": (ctypes.c_char_p, []),
@@ -556,3 +609,346 @@ def chunk_scan_varlen(cache: Cache, ssm: SSMParams, xBC: torch.Tensor, dt: torch
         _ptr(has_initial_state), _stream_ptr() if stream is None else stream)
     _check(st, "m2_chunk_scan_varlen_static" if static_scratch else "m2_chunk_scan_varlen")
     return y
+
+
+# ---- the 8-bit state cache ------------------------------------------------------
+
+def _need(ok: bool, what: str) -> None:
+    if not ok:
+        raise ValueError(what)
+
+
+def _rows(t: Optional[torch.Tensor], name: str, rows: int, width: int, dtype: torch.dtype,
+          device: torch.device) -> int:
+    """Checks a [rows, width] tensor (unit stride inside a row) and returns its row stride."""
+    if t is None:
+        return 0
+    _need(t.dtype == dtype, f"{name} must be {dtype}, not {t.dtype}")
+    _need(t.device == device, f"{name} is on {t.device}, the cache on {device}")
+    _need(t.dim() == 2 and t.shape[0] == rows and t.shape[1] == width,
+          f"{name} must be [{rows}, {width}], not {list(t.shape)}")
+    _need(t.stride(1) == 1, f"{name}: rows must be contiguous (unit stride in the last dimension)")
+    return t.stride(0) if rows > 1 else width
+
+
+def _index(t: torch.Tensor, name: str, n: int, device: torch.device) -> None:
+    _need(t.dtype == torch.int32 and t.is_contiguous() and t.numel() == n and t.device == device,
+          f"{name} must be {n} contiguous int32 on {device}")
+
+
+def _param(t: Optional[torch.Tensor], name: str, n: int, dtype: torch.dtype, device: torch.device) -> None:
+    if t is not None:
+        _need(t.dtype == dtype and t.is_contiguous() and t.numel() == n and t.device == device,
+              f"{name} must be {n} contiguous {dtype} on {device}")
+
+
+def _current(device: torch.device) -> None:
+    """The library launches on the current device: the cache has to be there."""
+    _need(device.type == "cuda" and device.index == torch.cuda.current_device(),
+          f"the cache is on {device}, which is not the current CUDA device")
+
+
+def _on(device: torch.device):
+    return torch.cuda.device(device) if device.type == "cuda" else contextlib.nullcontext()
+
+
+class Q8Cache:
+    """The state cache of a Mamba-2 mixer layer in 8 bits.
+
+    ``ssm`` int8 codes [num_slots, H, P, N], ``scale`` float32 [num_slots, H, P]
+    (a value is code * scale), ``conv`` [num_slots, K-1, conv_dim] activation
+    dtype, ``error`` a one-element int32 device word. ``shape.state_dtype`` is
+    not used. Slots start as zero states.
+    """
+
+    def __init__(self, shape: Shape, num_slots: int, device="cuda", ssm: Optional[torch.Tensor] = None,
+                 scale: Optional[torch.Tensor] = None, conv: Optional[torch.Tensor] = None):
+        self.shape = shape
+        self.num_slots = num_slots
+        dev = torch.device(device) if ssm is None else ssm.device
+        full = {"ssm": (ssm, (num_slots, shape.H, shape.P, shape.N), torch.int8),
+                "scale": (scale, (num_slots, shape.H, shape.P), torch.float32),
+                "conv": (conv, (num_slots, shape.K - 1, shape.conv_dim), torch_dtype(shape.act_dtype))}
+        for name, (t, size, dtype) in full.items():
+            if t is None:
+                t = torch.zeros(size, dtype=dtype, device=dev)
+                dev = t.device  # with its index
+            _need(t.dtype == dtype and tuple(t.shape) == size and t.is_contiguous() and t.device == dev,
+                  f"{name} must be contiguous {dtype} {list(size)} on {dev}")
+            setattr(self, name, t)
+        self.device = self.ssm.device
+        self.error = torch.zeros(1, dtype=torch.int32, device=dev)
+        self._c = m2_q8_cache()
+        s = shape.c()
+        with _on(self.device):
+            _check(lib().m2_q8_cache_wrap(ctypes.byref(s), num_slots, self.ssm.data_ptr(), self.scale.data_ptr(),
+                                          self.conv.data_ptr(), self.error.data_ptr(), ctypes.byref(self._c)),
+                   "m2_q8_cache_wrap")
+
+    @property
+    def c(self) -> m2_q8_cache:
+        return self._c
+
+    def zero_slots(self, slot_idx: torch.Tensor) -> None:
+        _current(self.device)
+        _index(slot_idx, "slot_idx", slot_idx.numel(), self.device)
+        _check(lib().m2_q8_zero_slots(ctypes.byref(self._c), slot_idx.numel(), slot_idx.data_ptr(), _stream_ptr()),
+               "m2_q8_zero_slots")
+
+    def device_error(self) -> int:
+        """Reads and clears the device error word (synchronises the stream)."""
+        _current(self.device)
+        code = _I32()
+        _check(lib().m2_q8_get_device_error(ctypes.byref(self._c), _stream_ptr(), ctypes.byref(code)),
+               "m2_q8_get_device_error")
+        return code.value
+
+
+def _q8_copy(name: str, src, dst, src_idx: torch.Tensor, dst_idx: torch.Tensor, stream: Optional[int]) -> None:
+    q8 = src if isinstance(src, Q8Cache) else dst
+    n = src_idx.numel()
+    _index(src_idx, "src_idx", n, q8.device)
+    _index(dst_idx, "dst_idx", n, q8.device)
+    full = dst if q8 is src else src
+    _need(full.ssm is None or full.ssm.device == q8.device, "the two caches are on different devices")
+    _current(q8.device)
+    _check(getattr(lib(), name)(ctypes.byref(src.c), ctypes.byref(dst.c), n, src_idx.data_ptr(), dst_idx.data_ptr(),
+                                _stream_ptr() if stream is None else stream), name)
+
+
+def q8_store(src: Cache, dst: Q8Cache, src_idx: torch.Tensor, dst_idx: torch.Tensor,
+             stream: Optional[int] = None) -> None:
+    """Quantises the states of ``src`` slots ``src_idx`` into ``dst`` slots
+    ``dst_idx`` (m2_q8_store); the conv rows are copied."""
+    _need(isinstance(src, Cache) and isinstance(dst, Q8Cache), "q8_store copies a Cache into a Q8Cache")
+    _q8_copy("m2_q8_store", src, dst, src_idx, dst_idx, stream)
+
+
+def q8_load(src: Q8Cache, dst: Cache, src_idx: torch.Tensor, dst_idx: torch.Tensor,
+            stream: Optional[int] = None) -> None:
+    """Reads ``src`` slots ``src_idx`` (which may repeat) back into ``dst`` slots
+    ``dst_idx`` (m2_q8_load)."""
+    _need(isinstance(src, Q8Cache) and isinstance(dst, Cache), "q8_load copies a Q8Cache into a Cache")
+    _q8_copy("m2_q8_load", src, dst, src_idx, dst_idx, stream)
+
+
+def q8_state_update(cache: Q8Cache, ssm: SSMParams, conv: ConvParams, xBC: torch.Tensor, dt: torch.Tensor,
+                    slot_idx: torch.Tensor, z: Optional[torch.Tensor] = None, y: Optional[torch.Tensor] = None,
+                    stream: Optional[int] = None, norm: Optional[NormParams] = None) -> torch.Tensor:
+    """One decode step in place on an 8-bit cache, the conv tap fused
+    (m2_q8_state_update; with ``norm`` the gated RMSNorm too). ``xBC`` [batch,
+    conv_dim] raw. Returns y [batch, H*P] in the activation dtype."""
+    sh, dev = cache.shape, cache.device
+    act = torch_dtype(sh.act_dtype)
+    batch, hp = xBC.shape[0], sh.H * sh.P
+    if y is None:
+        y = torch.empty((batch, hp), dtype=act, device=dev)
+    strides = [_rows(t, name, batch, width, act, dev)
+               for t, name, width in ((xBC, "xBC", sh.conv_dim), (dt, "dt", sh.H), (z, "z", hp), (y, "y", hp))]
+    _index(slot_idx, "slot_idx", batch, dev)
+    for t, name in ((ssm.A_log, "A_log"), (ssm.dt_bias, "dt_bias"), (ssm.D, "D")):
+        _param(t, name, sh.H, torch.float32, dev)
+    _param(conv.weight, "conv weight", sh.conv_dim * sh.K, act, dev)
+    _param(conv.bias, "conv bias", sh.conv_dim, act, dev)
+    if norm is not None:
+        _param(norm.weight, "norm weight", hp, act, dev)
+    _current(dev)
+    sp, cp = ssm.c(), conv.c()
+    rest = [batch, xBC.data_ptr(), strides[0], dt.data_ptr(), strides[1], _ptr(z), strides[2], y.data_ptr(), strides[3],
+            slot_idx.data_ptr(), _stream_ptr() if stream is None else stream]
+    if norm is not None:
+        npar = norm.c()
+        _check(lib().m2_q8_state_update_norm(ctypes.byref(cache.c), ctypes.byref(sp), ctypes.byref(cp),
+                                             ctypes.byref(npar), *rest), "m2_q8_state_update_norm")
+    else:
+        _check(lib().m2_q8_state_update(ctypes.byref(cache.c), ctypes.byref(sp), ctypes.byref(cp), *rest),
+               "m2_q8_state_update")
+    return y
+
+
+# ---- the per-channel selective scan ---------------------------------------------
+
+@dataclasses.dataclass(frozen=True)
+class SelShape:
+    """D channels of N states in G groups, a conv of K taps over the channels."""
+    D: int
+    N: int
+    G: int = 1
+    K: int = 4
+    state_dtype: int = M2_F32
+    act_dtype: int = M2_BF16
+
+    def c(self) -> m2_sel_shape:
+        return m2_sel_shape(self.D, self.N, self.G, self.K, self.state_dtype, self.act_dtype)
+
+
+def sel_shape_check(shape: SelShape) -> int:
+    s = shape.c()
+    return lib().m2_sel_shape_check(ctypes.byref(s))
+
+
+class SelCache:
+    """A slot-indexed state cache of one per-channel mixer layer: ``ssm``
+    [num_slots, D, N] state dtype, ``conv`` [num_slots, K-1, D] activation dtype
+    (last K-1 raw inputs, oldest row first), ``error`` as in ``Cache``."""
+
+    def __init__(self, shape: SelShape, num_slots: int, device="cuda", ssm: Optional[torch.Tensor] = None,
+                 conv: Optional[torch.Tensor] = None):
+        self.shape = shape
+        self.num_slots = num_slots
+        dev = torch.device(device) if ssm is None else ssm.device
+        full = {"ssm": (ssm, (num_slots, shape.D, shape.N), torch_dtype(shape.state_dtype)),
+                "conv": (conv, (num_slots, shape.K - 1, shape.D), torch_dtype(shape.act_dtype))}
+        for name, (t, size, dtype) in full.items():
+            if t is None:
+                t = torch.zeros(size, dtype=dtype, device=dev)
+                dev = t.device  # with its index
+            _need(t.dtype == dtype and tuple(t.shape) == size and t.is_contiguous() and t.device == dev,
+                  f"{name} must be contiguous {dtype} {list(size)} on {dev}")
+            setattr(self, name, t)
+        self.device = self.ssm.device
+        self.error = torch.zeros(1, dtype=torch.int32, device=dev)
+        self._c = m2_sel_cache()
+        s = shape.c()
+        with _on(self.device):
+            _check(lib().m2_sel_cache_wrap(ctypes.byref(s), num_slots, self.ssm.data_ptr(), self.conv.data_ptr(),
+                                           self.error.data_ptr(), ctypes.byref(self._c)), "m2_sel_cache_wrap")
+
+    @property
+    def c(self) -> m2_sel_cache:
+        return self._c
+
+    def zero_slots(self, slot_idx: torch.Tensor) -> None:
+        _current(self.device)
+        _index(slot_idx, "slot_idx", slot_idx.numel(), self.device)
+        _check(lib().m2_sel_zero_slots(ctypes.byref(self._c), slot_idx.numel(), slot_idx.data_ptr(), _stream_ptr()),
+               "m2_sel_zero_slots")
+
+    def device_error(self) -> int:
+        """Reads and clears the device error word (synchronises the stream)."""
+        _current(self.device)
+        code = _I32()
+        _check(lib().m2_sel_get_device_error(ctypes.byref(self._c), _stream_ptr(), ctypes.byref(code)),
+               "m2_sel_get_device_error")
+        return code.value
+
+
+@dataclasses.dataclass
+class SelParams:
+    """fp32 parameters: A_log [D, N] (A = -exp(A_log)), dt_bias [D], D [D]."""
+    A_log: torch.Tensor
+    dt_bias: torch.Tensor
+    D: torch.Tensor
+
+    def c(self, shape: SelShape, device: torch.device) -> m2_sel_params:
+        _param(self.A_log, "A_log", shape.D * shape.N, torch.float32, device)
+        _param(self.dt_bias, "dt_bias", shape.D, torch.float32, device)
+        _param(self.D, "D", shape.D, torch.float32, device)
+        return m2_sel_params(self.A_log.data_ptr(), self.dt_bias.data_ptr(), self.D.data_ptr())
+
+
+def _sel_rows(cache: SelCache, x, dt, B, C, z, y) -> list:
+    """Pointers and row strides of a per-channel call's tensors, checked."""
+    sh, dev = cache.shape, cache.device
+    act = torch_dtype(sh.act_dtype)
+    T, gn = x.shape[0], sh.G * sh.N
+    out = []
+    for t, name, width in ((x, "x", sh.D), (dt, "dt", sh.D), (B, "B", gn), (C, "C", gn), (z, "z", sh.D), (y, "y", sh.D)):
+        if t is not None and t.dim() == 3 and name in "BC":  # [T, G, N]: a row is its G*N values
+            _need(t.shape[1:] == (sh.G, sh.N) and t.stride(2) == 1 and (sh.G == 1 or t.stride(1) == sh.N),
+                  f"{name} must be [{T}, {sh.G}, {sh.N}] with contiguous rows, not {list(t.shape)}")
+            t = t.as_strided((t.shape[0], gn), (t.stride(0), 1))
+        stride = _rows(t, name, T, width, act, dev)
+        out += [_ptr(t), stride]
+    return out
+
+
+def sel_state_update(cache: SelCache, params: SelParams, x: torch.Tensor, dt: torch.Tensor, B: torch.Tensor,
+                     C: torch.Tensor, slot_idx: torch.Tensor, z: Optional[torch.Tensor] = None,
+                     y: Optional[torch.Tensor] = None, stream: Optional[int] = None) -> torch.Tensor:
+    """One token per row of the per-channel selective scan, in place on
+    ``cache`` (m2_sel_state_update): x (post-conv), dt, z [batch, D], B and C
+    [batch, G, N]. Returns y [batch, D]."""
+    if y is None:
+        y = torch.empty((x.shape[0], cache.shape.D), dtype=torch_dtype(cache.shape.act_dtype), device=cache.device)
+    rows = _sel_rows(cache, x, dt, B, C, z, y)
+    _index(slot_idx, "slot_idx", x.shape[0], cache.device)
+    sp = params.c(cache.shape, cache.device)
+    _current(cache.device)
+    _check(lib().m2_sel_state_update(ctypes.byref(cache.c), ctypes.byref(sp), x.shape[0], *rows, slot_idx.data_ptr(),
+                                     _stream_ptr() if stream is None else stream), "m2_sel_state_update")
+    return y
+
+
+def sel_scan(cache: SelCache, params: SelParams, x: torch.Tensor, dt: torch.Tensor, B: torch.Tensor, C: torch.Tensor,
+             cu_seqlens: torch.Tensor, slot_idx: torch.Tensor, max_seqlen: Optional[int] = None,
+             z: Optional[torch.Tensor] = None, has_initial_state: Optional[torch.Tensor] = None,
+             y: Optional[torch.Tensor] = None, stream: Optional[int] = None) -> torch.Tensor:
+    """Prompts packed back to back through the per-channel selective scan
+    (m2_sel_scan): x (post-conv), dt, z [total, D], B and C [total, G, N],
+    cu_seqlens [nseq+1] int32. ``max_seqlen`` (a bound on the lengths) is
+    ``total`` when None. Returns y [total, D]."""
+    dev = cache.device
+    nseq = cu_seqlens.numel() - 1
+    _need(nseq >= 0, "cu_seqlens must hold nseq + 1 offsets")
+    if y is None:
+        y = torch.empty((x.shape[0], cache.shape.D), dtype=torch_dtype(cache.shape.act_dtype), device=dev)
+    rows = _sel_rows(cache, x, dt, B, C, z, y)
+    _index(cu_seqlens, "cu_seqlens", nseq + 1, dev)
+    _index(slot_idx, "slot_idx", nseq, dev)
+    if has_initial_state is not None:
+        _param(has_initial_state, "has_initial_state", nseq, has_initial_state.dtype, dev)
+        _need(has_initial_state.dtype in (torch.uint8, torch.bool), "has_initial_state must be uint8 or bool")
+    sp = params.c(cache.shape, dev)
+    _current(dev)
+    _check(lib().m2_sel_scan(ctypes.byref(cache.c), ctypes.byref(sp), nseq, cu_seqlens.data_ptr(), x.shape[0],
+                             x.shape[0] if max_seqlen is None else max_seqlen, *rows, slot_idx.data_ptr(),
+                             _ptr(has_initial_state), _stream_ptr() if stream is None else stream), "m2_sel_scan")
+    return y
+
+
+def _sel_conv_args(cache: SelCache, conv: ConvParams, x: torch.Tensor, out: Optional[torch.Tensor],
+                   out_dtype: Optional[torch.dtype]):
+    sh, dev = cache.shape, cache.device
+    act = torch_dtype(sh.act_dtype)
+    if out is None:
+        out = torch.empty(x.shape, dtype=out_dtype or act, device=dev)
+    _param(conv.weight, "conv weight", sh.D * sh.K, act, dev)
+    _param(conv.bias, "conv bias", sh.D, act, dev)
+    return out, _rows(x, "x", x.shape[0], sh.D, act, dev), _rows(out, "out", x.shape[0], sh.D, out.dtype, dev)
+
+
+def sel_conv1d_update(cache: SelCache, conv: ConvParams, x: torch.Tensor, slot_idx: torch.Tensor,
+                      out: Optional[torch.Tensor] = None, out_dtype: Optional[torch.dtype] = None,
+                      stream: Optional[int] = None) -> torch.Tensor:
+    """The causal conv tap for one token per row, x [batch, D]
+    (m2_sel_conv1d_update with one token a row); rolls ``cache.conv``."""
+    out, xs, os_ = _sel_conv_args(cache, conv, x, out, out_dtype)
+    _index(slot_idx, "slot_idx", x.shape[0], cache.device)
+    cp = conv.c()
+    _current(cache.device)
+    _check(lib().m2_sel_conv1d_update(ctypes.byref(cache.c), ctypes.byref(cp), x.shape[0], 1, x.data_ptr(), xs,
+                                      out.data_ptr(), _dtype_code(out.dtype), os_, slot_idx.data_ptr(),
+                                      _stream_ptr() if stream is None else stream), "m2_sel_conv1d_update")
+    return out
+
+
+def sel_conv1d_update_varlen(cache: SelCache, conv: ConvParams, x: torch.Tensor, cu_seqlens: torch.Tensor,
+                             slot_idx: torch.Tensor, max_seqlen: Optional[int] = None,
+                             out: Optional[torch.Tensor] = None, out_dtype: Optional[torch.dtype] = None,
+                             stream: Optional[int] = None) -> torch.Tensor:
+    """The causal conv over prompts packed back to back, x [total, D]
+    (m2_sel_conv1d_update_varlen); rolls ``cache.conv``."""
+    out, xs, os_ = _sel_conv_args(cache, conv, x, out, out_dtype)
+    nseq = cu_seqlens.numel() - 1
+    _need(nseq >= 0, "cu_seqlens must hold nseq + 1 offsets")
+    _index(cu_seqlens, "cu_seqlens", nseq + 1, cache.device)
+    _index(slot_idx, "slot_idx", nseq, cache.device)
+    cp = conv.c()
+    _current(cache.device)
+    _check(lib().m2_sel_conv1d_update_varlen(ctypes.byref(cache.c), ctypes.byref(cp), nseq, cu_seqlens.data_ptr(),
+                                             x.shape[0], x.shape[0] if max_seqlen is None else max_seqlen,
+                                             x.data_ptr(), xs, out.data_ptr(), _dtype_code(out.dtype), os_,
+                                             slot_idx.data_ptr(), _stream_ptr() if stream is None else stream),
+           "m2_sel_conv1d_update_varlen")
+    return out

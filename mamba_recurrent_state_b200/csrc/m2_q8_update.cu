@@ -1,0 +1,467 @@
+// m2_q8_update.cu -- the one-token decode step on an 8-bit state cache: the
+// conv tap and the selective state update of m2_state_update.cu, with the
+// state read as codes * scale, updated in fp32 and stored as codes and a new
+// scale per row, all in one launch. Per head h, group g = h / (H/G):
+//   S = code * scale, S' = S*dA + (dt*x)*B[g], y = sum_n S'*C[g] + D*x
+//   a = max_n |S'|, scale' = a / 127, code' = rne(S' * (127 / a))
+// y comes from the unrounded S'. All of it is fp32 between the codes.
+//
+// Work decomposition:
+//  * A sequence's state is H*P rows of N codes. The rows of an SSM group are
+//    cut into tiles of tile_rows rows (the last may be short), a CTA of 256
+//    threads each, the group's CTAs one thread-block cluster.
+//  * One thread puts the slot's conv rows, the tile's scales and the codes in
+//    flight as bulk copies before anything else is computed.
+//  * LPR = N/16 lanes share a row, 16 codes (one 16-byte vector) a lane. A
+//    thread works on two rows at once: their S' stay in registers while the
+//    sums y and the maxima a go over the LPR lanes, both with the first level
+//    exchanging halves, so that one lane in two ends with one row's result and
+//    divides for one row only; the inverses come back with one shuffle a row.
+//  * Codes become floats by a byte permute into 2^23 and one exact subtraction
+//    and are rounded by one FMA with 1.5 * 2^23 (m2_q8.cuh): no conversion
+//    instructions, which issue at a quarter of the FMA rate.
+//  * Conv, cluster and waits as in m2_state_update.cu: every CTA computes the
+//    conv of its x channels and of the group's B and C; cluster rank 0 alone
+//    rolls the group's B/C conv rows, after all have read them.
+#include <cuda_runtime.h>
+
+#include <algorithm>
+
+#include "m2_q8.cuh"
+
+namespace m2 {
+namespace {
+
+constexpr int kThreads = 256;
+constexpr int kWarps = kThreads / 32;
+constexpr int kRowsPerThread = 2;
+constexpr int kMaxPasses = 8;       // passes of a CTA over its tile, one barrier each
+constexpr int kMaxHeads = 66;       // heads that a tile of 512 rows can touch (P >= 8)
+constexpr int kMaxCluster = 16;
+constexpr uint64_t kWaitLimitNs = 1000000000ull;
+
+__device__ __forceinline__ void cluster_arrive_relaxed() {
+    asm volatile("barrier.cluster.arrive.relaxed.aligned;\n" ::: "memory");
+}
+__device__ __forceinline__ void cluster_arrive_release() {
+    asm volatile("barrier.cluster.arrive.release.aligned;\n" ::: "memory");
+}
+__device__ __forceinline__ void cluster_wait() {
+    asm volatile("barrier.cluster.wait.acquire.aligned;\n" ::: "memory");
+}
+__device__ __forceinline__ uint32_t cluster_rank() {
+    uint32_t r;
+    asm volatile("mov.u32 %0, %%cluster_ctarank;\n" : "=r"(r));
+    return r;
+}
+__device__ __forceinline__ void st_cluster_f32(float* local, uint32_t rank, float v) {
+    uint32_t remote;
+    asm volatile("mapa.shared::cluster.u32 %0, %1, %2;\n" : "=r"(remote) : "r"(smem_addr(local)), "r"(rank));
+    asm volatile("st.shared::cluster.f32 [%0], %1;\n" ::"r"(remote), "f"(v) : "memory");
+}
+
+// One 32-bit word of activations: two bf16 channels or one fp32.
+template <typename AT>
+__device__ __forceinline__ void unpack_word(uint32_t u, float* out) {
+    if constexpr (sizeof(AT) == 2) {
+        out[0] = __uint_as_float(u << 16);
+        out[1] = __uint_as_float(u & 0xFFFF0000u);
+    } else {
+        out[0] = __uint_as_float(u);
+    }
+}
+
+// Byte offsets of the dynamic shared memory of a CTA.
+struct Layout {
+    int scale, conv_x, conv_bc, rp, y, nscale, B, C, raw_bc, bytes;
+    __host__ __device__ Layout(int tile, int N, int K, int as) {
+        scale = tile * N;                       // old scales
+        conv_x = scale + tile * 4;              // [K-1][tile]
+        conv_bc = conv_x + (K - 1) * tile * as; // [2][K-1][N]
+        rp = conv_bc + 2 * (K - 1) * N * as;    // per row {dt*x, scale*dA, D*x, -}
+        y = rp + tile * 16;
+        nscale = y + tile * 4;
+        B = nscale + tile * 4;
+        C = B + N * 4;
+        raw_bc = C + N * 4;                     // this step's raw B and C inputs
+        bytes = raw_bc + 2 * N * as;
+    }
+};
+
+// The sum (or largest) of two rows over their LPR lanes: lanes with the upper
+// half bit end with row 1, the others with row 0.
+template <int LPR, typename Op>
+__device__ __forceinline__ float reduce_two(float v0, float v1, bool upper, Op op) {
+    float v = op(upper ? v1 : v0, __shfl_xor_sync(0xffffffffu, upper ? v0 : v1, LPR / 2));
+#pragma unroll
+    for (int off = LPR / 4; off > 0; off >>= 1) v = op(v, __shfl_xor_sync(0xffffffffu, v, off));
+    return v;
+}
+
+template <typename AT, int N, bool NORM>
+__global__ void __launch_bounds__(kThreads, 2) q8_update_kernel(const Q8UpdateArgs a) {
+    constexpr int LPR = N / 16;
+    constexpr int RPP = kThreads / LPR;              // rows a CTA covers once
+    constexpr int PASS = RPP * kRowsPerThread;       // rows of one pass
+    constexpr int CW = 4 / sizeof(AT);               // channels per 32-bit word
+    constexpr int AS = sizeof(AT);
+
+    extern __shared__ __align__(128) uint8_t s_dyn[];
+    __shared__ __align__(8) uint64_t s_bar[kMaxPasses + 1];
+    __shared__ float s_dt[kMaxHeads], s_dA[kMaxHeads], s_D[kMaxHeads];
+    __shared__ int s_fail;
+    __shared__ float s_red[kWarps], s_parts[kMaxCluster], s_rstd;
+
+    const int tid = threadIdx.x;
+    const int K = a.K, P = a.P;
+    const int64_t HP = static_cast<int64_t>(a.H) * P;
+    const int group_rows = a.H / a.G * P;
+    const int g = blockIdx.x / a.group_ctas;
+    const int off = (blockIdx.x % a.group_ctas) * a.tile_rows;  // first row within the group
+    const int nrows = min(a.tile_rows, group_rows - off);       // a multiple of 8, at least 8
+    const int64_t r0 = static_cast<int64_t>(g) * group_rows + off;
+    const int h_first = static_cast<int>(r0 / P);
+    const int rr0 = static_cast<int>(r0 - static_cast<int64_t>(h_first) * P);
+    const int n_heads = (rr0 + nrows - 1) / P + 1;
+    const int64_t cd = a.conv_dim;
+    const int64_t cB = HP + static_cast<int64_t>(g) * N;
+    const int64_t cC = cB + static_cast<int64_t>(a.G) * N;
+    const Layout L(a.tile_rows, N, K, AS);
+    const uint8_t* s_codes = s_dyn;
+    const float* s_scale = reinterpret_cast<const float*>(s_dyn + L.scale);
+    const AT* s_cx = reinterpret_cast<const AT*>(s_dyn + L.conv_x);
+    const AT* s_cbc = reinterpret_cast<const AT*>(s_dyn + L.conv_bc);
+    float4* s_rp = reinterpret_cast<float4*>(s_dyn + L.rp);
+    float* s_y = reinterpret_cast<float*>(s_dyn + L.y);
+    float* s_nscale = reinterpret_cast<float*>(s_dyn + L.nscale);
+    float* s_B = reinterpret_cast<float*>(s_dyn + L.B);
+    float* s_C = reinterpret_cast<float*>(s_dyn + L.C);
+    uint32_t* s_rawbc = reinterpret_cast<uint32_t*>(s_dyn + L.raw_bc);
+
+    // A programmatic dependent of the previous kernel: nothing is read before.
+    asm volatile("griddepcontrol.wait;\n" ::: "memory");
+
+    const int64_t b = blockIdx.y;
+    const AT* xrow = static_cast<const AT*>(a.xBC) + b * a.xBC_stride;
+    const AT* zrow = a.z ? static_cast<const AT*>(a.z) + b * a.z_stride : nullptr;
+    AT* yrow = static_cast<AT*>(a.y) + b * a.y_stride;
+    const int32_t slot = a.slot_idx[b];
+    // skipped rows are skipped by the whole cluster
+    if (slot < 0) {
+        for (int i = tid; i < nrows; i += kThreads) yrow[r0 + i] = from_f32<AT>(0.f);
+        return;
+    }
+    if (slot >= a.num_slots) {
+        if (tid == 0) record_error(a.error, M2_ERR_BAD_SLOT);
+        return;
+    }
+    const int64_t row_base = static_cast<int64_t>(slot) * HP + r0;
+    int8_t* tile = a.ssm + row_base * N;
+    float* scales = a.scale + row_base;
+    AT* conv0 = static_cast<AT*>(a.conv) + static_cast<int64_t>(slot) * (K - 1) * cd;
+    uint64_t* bar_conv = &s_bar[kMaxPasses];
+    const int passes = (nrows + PASS - 1) / PASS;
+    if (tid == 0) {
+        s_fail = 0;
+        for (int c = 0; c <= kMaxPasses; ++c) mbar_init(&s_bar[c], 1);
+        fence_mbar_init();
+        mbar_arrive_expect_tx(bar_conv, static_cast<uint32_t>((K - 1) * (nrows + 2 * N) * AS + nrows * 4));
+        bulk_g2s(s_dyn + L.scale, scales, nrows * 4, bar_conv);
+        for (int k = 0; k < K - 1; ++k) {
+            bulk_g2s(s_dyn + L.conv_x + k * a.tile_rows * AS, conv0 + k * cd + r0, nrows * AS, bar_conv);
+            bulk_g2s(s_dyn + L.conv_bc + k * N * AS, conv0 + k * cd + cB, N * AS, bar_conv);
+            bulk_g2s(s_dyn + L.conv_bc + (K - 1 + k) * N * AS, conv0 + k * cd + cC, N * AS, bar_conv);
+        }
+        for (int c = 0; c < passes; ++c) {
+            const int rows = min(PASS, nrows - c * PASS);
+            mbar_arrive_expect_tx(&s_bar[c], rows * N);
+            bulk_g2s(s_dyn + c * PASS * N, tile + static_cast<int64_t>(c) * PASS * N, rows * N, &s_bar[c]);
+        }
+    }
+    asm volatile("griddepcontrol.launch_dependents;\n" ::: "memory");
+    if (tid < n_heads) {
+        const int h = h_first + tid;
+        const float dt = softplus_f32(to_f32(static_cast<const AT*>(a.dt)[b * a.dt_stride + h]) + a.dt_bias[h]);
+        s_dt[tid] = dt;
+        s_dA[tid] = expf(dt * -expf(a.A_log[h]));
+        s_D[tid] = a.D[h];
+    }
+    __syncthreads();
+
+    // ---- conv: one word of channels at a time, x of the tile, then B and C
+    {
+        const AT* w = static_cast<const AT*>(a.conv_w);
+        const AT* bias = static_cast<const AT*>(a.conv_b);
+        const int nx = nrows / CW;
+        for (int q = tid; q < nx + 2 * N / CW; q += kThreads) {
+            const bool is_x = q < nx;
+            const int j = is_x ? q * CW : (q - nx) * CW;  // channel within the segment(s)
+            const int seg = j / N;                        // (B, C) 0 or 1
+            const int64_t c0 = is_x ? r0 + j : (seg ? cC : cB) + (j - seg * N);
+            const AT* rows = is_x ? s_cx + j : s_cbc + seg * (K - 1) * N + (j - seg * N);
+            const int pitch = is_x ? a.tile_rows : N;
+            const uint32_t raw = *reinterpret_cast<const uint32_t*>(xrow + c0);
+            float out[CW], xv[CW];
+            unpack_word<AT>(bias ? __ldg(reinterpret_cast<const uint32_t*>(bias + c0)) : 0u, out);
+            unpack_word<AT>(raw, xv);
+            float w4[CW * 4];
+            if (K == 4) {  // the CW x 4 weights are one 16-byte vector
+                float t[Vec16<AT>::n];
+                unpack16<AT>(__ldg(reinterpret_cast<const uint4*>(w + c0 * 4)), t);
+#pragma unroll
+                for (int i = 0; i < CW * 4; ++i) w4[i] = t[i];
+            }
+            if (!mbar_wait_bounded(bar_conv, 0, kWaitLimitNs)) {
+                record_error(a.error, M2_ERR_TIMEOUT);
+                s_fail = 1;
+                break;
+            }
+            if (K == 4) {
+#pragma unroll
+                for (int k = 0; k < 3; ++k) {
+                    float rv[CW];
+                    unpack_word<AT>(*reinterpret_cast<const uint32_t*>(rows + k * pitch), rv);
+#pragma unroll
+                    for (int e = 0; e < CW; ++e) out[e] = fmaf(w4[e * 4 + k], rv[e], out[e]);
+                }
+#pragma unroll
+                for (int e = 0; e < CW; ++e) out[e] = fmaf(w4[e * 4 + 3], xv[e], out[e]);
+            } else {
+                for (int k = 0; k < K; ++k) {
+                    float rv[CW];
+                    unpack_word<AT>(k < K - 1 ? *reinterpret_cast<const uint32_t*>(rows + k * pitch) : raw, rv);
+#pragma unroll
+                    for (int e = 0; e < CW; ++e) out[e] = fmaf(to_f32(__ldg(w + (c0 + e) * K + k)), rv[e], out[e]);
+                }
+            }
+            if (a.activation) {
+#pragma unroll
+                for (int e = 0; e < CW; ++e) out[e] = silu_f32(out[e]);
+            }
+            if (is_x) {
+                for (int k = 0; k < K - 1; ++k)  // roll this CTA's own conv rows
+                    *reinterpret_cast<uint32_t*>(conv0 + k * cd + c0) =
+                        k < K - 2 ? *reinterpret_cast<const uint32_t*>(rows + (k + 1) * pitch) : raw;
+                const int hl = (rr0 + j) / P;  // CW channels lie in one head
+                const float dtv = s_dt[hl], dAv = s_dA[hl], Dv = s_D[hl];
+#pragma unroll
+                for (int e = 0; e < CW; ++e)
+                    s_rp[j + e] = make_float4(dtv * out[e], s_scale[j + e] * dAv, Dv * out[e], 0.f);
+            } else {
+                float* dst = (seg ? s_C : s_B) + (j - seg * N);
+#pragma unroll
+                for (int e = 0; e < CW; ++e) dst[e] = out[e];
+                s_rawbc[j / CW] = raw;
+            }
+        }
+        cluster_arrive_relaxed();  // this CTA has read the group's B/C conv rows
+    }
+    __syncthreads();
+    bool ok = s_fail == 0;
+
+    // ---- the state, two rows a thread at a time
+    const int lane = tid & 31;
+    const int l = lane % LPR;
+    const bool upper = (lane & (LPR / 2)) != 0;
+    float2 B2[8], C2[8];
+#pragma unroll
+    for (int e = 0; e < 8; ++e) {
+        B2[e] = *reinterpret_cast<const float2*>(s_B + l * 16 + 2 * e);
+        C2[e] = *reinterpret_cast<const float2*>(s_C + l * 16 + 2 * e);
+    }
+#pragma unroll 1
+    for (int c = 0; c < passes && ok; ++c) {
+        if (!mbar_wait_bounded(&s_bar[c], 0, kWaitLimitNs)) {
+            record_error(a.error, M2_ERR_TIMEOUT);
+            ok = false;
+            break;
+        }
+        float2 S[kRowsPerThread][8];
+        float sum[kRowsPerThread], big[kRowsPerThread];
+#pragma unroll
+        for (int i = 0; i < kRowsPerThread; ++i) {
+            const int row = c * PASS + i * RPP + tid / LPR;  // < tile_rows
+            const float4 rp = s_rp[row];
+            const uint4 w = *reinterpret_cast<const uint4*>(s_codes + row * N + l * 16);
+            const uint32_t words[4] = {w.x, w.y, w.z, w.w};
+            const float2 dtx = make_float2(rp.x, rp.x), k2 = make_float2(rp.y, rp.y);
+            float2 acc = make_float2(0.f, 0.f);
+            float m = 0.f;
+#pragma unroll
+            for (int q = 0; q < 4; ++q) {
+                float2 lo, hi;
+                q8_unpack(words[q], lo, hi);
+                lo = __ffma2_rn(lo, k2, __fmul2_rn(dtx, B2[2 * q]));
+                hi = __ffma2_rn(hi, k2, __fmul2_rn(dtx, B2[2 * q + 1]));
+                acc = __ffma2_rn(lo, C2[2 * q], acc);
+                acc = __ffma2_rn(hi, C2[2 * q + 1], acc);
+                m = max_nan(max_nan(m, fabsf(lo.x)), fabsf(lo.y));
+                m = max_nan(max_nan(m, fabsf(hi.x)), fabsf(hi.y));
+                S[i][2 * q] = lo;
+                S[i][2 * q + 1] = hi;
+            }
+            sum[i] = acc.x + acc.y;
+            big[i] = m;
+        }
+        const float ysum = reduce_two<LPR>(sum[0], sum[1], upper, [](float u, float v) { return u + v; });
+        const float amax = reduce_two<LPR>(big[0], big[1], upper, [](float u, float v) { return max_nan(u, v); });
+        float scale, inv;
+        q8_scale(amax, scale, inv);
+        if (l % (LPR / 2) == 0) {
+            const int row = c * PASS + (upper ? RPP : 0) + tid / LPR;
+            if (row < nrows) {
+                s_y[row] = ysum + s_rp[row].z;
+                s_nscale[row] = scale;
+            }
+        }
+        float inv_of[kRowsPerThread];
+        inv_of[0] = __shfl_sync(0xffffffffu, inv, lane & ~(LPR / 2));
+        inv_of[1] = __shfl_sync(0xffffffffu, inv, lane | (LPR / 2));
+#pragma unroll
+        for (int i = 0; i < kRowsPerThread; ++i) {
+            const int row = c * PASS + i * RPP + tid / LPR;
+            const float2 iv = make_float2(inv_of[i], inv_of[i]), mg = make_float2(kQ8Magic, kQ8Magic);
+            uint32_t out[4];
+#pragma unroll
+            for (int q = 0; q < 4; ++q) {
+                const float2 lo = __ffma2_rn(S[i][2 * q], iv, mg), hi = __ffma2_rn(S[i][2 * q + 1], iv, mg);
+                out[q] = q8_pack(lo.x, lo.y, hi.x, hi.y);
+            }
+            if (row < nrows)
+                st_stream(tile + static_cast<int64_t>(row) * N + l * 16, make_uint4(out[0], out[1], out[2], out[3]));
+        }
+    }
+    if (!ok) {  // let this CTA's copies land before its shared memory goes
+        for (int c = 0; c < passes; ++c) mbar_wait_bounded(&s_bar[c], 0, kWaitLimitNs);
+        mbar_wait_bounded(bar_conv, 0, kWaitLimitNs);
+    }
+    __syncthreads();
+
+    if (ok) {
+        for (int i = tid; i < nrows; i += kThreads) scales[i] = s_nscale[i];
+    }
+    if constexpr (!NORM) {
+        if (ok) {
+            for (int i = tid; i < nrows; i += kThreads) {
+                float yv = s_y[i];
+                if (zrow) yv *= silu_f32(to_f32(zrow[r0 + i]));
+                yrow[r0 + i] = from_f32<AT>(yv);
+            }
+        }
+    } else {
+        // gated RMSNorm over the group's rows, which are this cluster's
+        float ss = 0.f;
+        if (ok) {
+            for (int i = tid; i < nrows; i += kThreads) {
+                float yv = s_y[i];
+                if (zrow) yv *= silu_f32(to_f32(zrow[r0 + i]));
+                s_y[i] = yv;
+                ss = fmaf(yv, yv, ss);
+            }
+        }
+#pragma unroll
+        for (int o = 16; o > 0; o >>= 1) ss += __shfl_xor_sync(0xffffffffu, ss, o);
+        if (lane == 0) s_red[tid >> 5] = ss;
+        __syncthreads();
+        cluster_wait();  // the phase of the conv's arrive: every CTA is running
+        if (tid < a.group_ctas) {
+            float part = 0.f;
+            for (int w = 0; w < kWarps; ++w) part += s_red[w];
+            st_cluster_f32(&s_parts[cluster_rank()], static_cast<uint32_t>(tid), part);
+        }
+        cluster_arrive_release();
+        cluster_wait();
+        if (tid == 0) {
+            float total = 0.f;
+            for (int q = 0; q < a.group_ctas; ++q) total += s_parts[q];
+            s_rstd = rsqrtf(total / static_cast<float>(group_rows) + a.norm_eps);
+        }
+        __syncthreads();
+        if (ok) {
+            const AT* nw = static_cast<const AT*>(a.norm_w);
+            for (int i = tid; i < nrows; i += kThreads)
+                yrow[r0 + i] = from_f32<AT>(s_y[i] * s_rstd * to_f32(nw[r0 + i]));
+        }
+    }
+
+    // ---- cluster rank 0 rolls the group's B and C conv rows
+    if (!NORM && cluster_rank() == 0) cluster_wait();
+    if (ok && cluster_rank() == 0) {
+        for (int q = tid; q < 2 * N / CW; q += kThreads) {
+            const int j = q * CW, seg = j / N;
+            const int64_t c0 = (seg ? cC : cB) + (j - seg * N);
+            const AT* rows = s_cbc + seg * (K - 1) * N + (j - seg * N);
+            for (int k = 0; k < K - 1; ++k)
+                *reinterpret_cast<uint32_t*>(conv0 + k * cd + c0) =
+                    k < K - 2 ? *reinterpret_cast<const uint32_t*>(rows + (k + 1) * N) : s_rawbc[q];
+        }
+    }
+}
+
+template <typename AT, int N, bool NORM>
+cudaError_t launch_one(const Q8UpdateArgs& a, cudaStream_t stream) {
+    auto kern = q8_update_kernel<AT, N, NORM>;
+    static AttrOnce attrs;
+    const cudaError_t e = attrs.ensure([&] {
+        cudaError_t r = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, 160 * 1024);
+        if (r == cudaSuccess) r = cudaFuncSetAttribute(kern, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
+        return r;
+    });
+    if (e != cudaSuccess) return e;
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(a.G * a.group_ctas, a.batch, 1);
+    cfg.blockDim = dim3(kThreads, 1, 1);
+    cfg.dynamicSmemBytes = Layout(a.tile_rows, N, a.K, sizeof(AT)).bytes;
+    cfg.stream = stream;
+    cudaLaunchAttribute attr[2];
+    attr[0].id = cudaLaunchAttributeClusterDimension;
+    attr[0].val.clusterDim.x = a.group_ctas;
+    attr[0].val.clusterDim.y = 1;
+    attr[0].val.clusterDim.z = 1;
+    attr[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[1].val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 2;
+    return cudaLaunchKernelEx(&cfg, kern, a);
+}
+
+template <typename AT, int N>
+cudaError_t by_norm(const Q8UpdateArgs& a, cudaStream_t s) {
+    return a.norm_w ? launch_one<AT, N, true>(a, s) : launch_one<AT, N, false>(a, s);
+}
+
+template <typename AT>
+cudaError_t by_n(const Q8UpdateArgs& a, cudaStream_t s) {
+    switch (a.N) {
+        case 64: return by_norm<AT, 64>(a, s);
+        case 128: return by_norm<AT, 128>(a, s);
+        case 256: return by_norm<AT, 256>(a, s);
+        default: return cudaErrorInvalidValue;
+    }
+}
+
+// Rows of one pass and the largest tile of a CTA.
+int pass_rows(int N) { return kThreads / (N / 16) * kRowsPerThread; }
+int max_tile(int N) { return std::min(512, pass_rows(N) * kMaxPasses); }
+
+}  // namespace
+
+m2_status q8_shape_supported(int H, int P, int N, int G) {
+    if (N != 64 && N != 128 && N != 256) return M2_ERR_UNSUPPORTED;
+    if (P < 8 || P > 256 || P % 8 != 0) return M2_ERR_UNSUPPORTED;
+    const int64_t group_rows = static_cast<int64_t>(H / G) * P;
+    if (group_rows > static_cast<int64_t>(kMaxCluster) * max_tile(N)) return M2_ERR_UNSUPPORTED;
+    return M2_OK;
+}
+
+cudaError_t launch_q8_update(Q8UpdateArgs a, cudaStream_t stream) {
+    const int group_rows = a.H / a.G * a.P;
+    int tile = std::min(256, max_tile(a.N));
+    if (group_rows < tile) tile = (group_rows + pass_rows(a.N) - 1) / pass_rows(a.N) * pass_rows(a.N);
+    while ((group_rows + tile - 1) / tile > kMaxCluster) tile *= 2;
+    a.tile_rows = tile;
+    a.group_ctas = (group_rows + tile - 1) / tile;
+    return a.act_bf16 ? by_n<bf16_t>(a, stream) : by_n<float>(a, stream);
+}
+
+}  // namespace m2
