@@ -92,6 +92,25 @@ __device__ __forceinline__ void q8_scale(float a, float& scale, float& inv) {
     scale = live ? __fdiv_rn(d, 127.f) : (finite ? 0.f : __int_as_float(0x7fc00000));
 }
 
+// The largest of m and the magnitudes of a and b; a NaN stays.
+__device__ __forceinline__ float max_abs(float m, float a, float b) {
+    float r;
+    asm("max.NaN.abs.f32 %0, %1, %2, %3;" : "=f"(r) : "f"(m), "f"(a), "f"(b));
+    return r;
+}
+
+// q8_scale for the decode step: a product with 1/127 and the reciprocal of the
+// special-function unit, each within 2^-22 of the quotient. It takes the
+// quotients only where the reciprocal would leave the normal range.
+__device__ __forceinline__ void q8_scale_fast(float a, float& scale, float& inv) {
+    if (a >= 7.888609052e-31f && a <= 1.329227996e36f) {  // 2^-100 .. 2^120
+        scale = a * (1.f / 127.f);
+        inv = 127.f * rcp_approx(a);
+    } else {
+        q8_scale(a, scale, inv);
+    }
+}
+
 // 1.5 * 2^23: fma(v, inv, kQ8Magic) rounds the exact product half to even to
 // an integer k, |k| < 2^22, and its low byte is k in two's complement.
 constexpr float kQ8Magic = 12582912.f;

@@ -32,10 +32,24 @@
 namespace m2 {
 namespace {
 
-constexpr int kThreads = 256;
+#ifndef Q8_THREADS
+#define Q8_THREADS 128
+#endif
+#ifndef Q8_MINB
+#define Q8_MINB 4
+#endif
+#ifndef Q8_CP
+#define Q8_CP 4
+#endif
+#ifndef Q8_TILE
+#define Q8_TILE 256
+#endif
+constexpr int kThreads = Q8_THREADS;
 constexpr int kWarps = kThreads / 32;
 constexpr int kRowsPerThread = 2;
-constexpr int kMaxPasses = 8;       // passes of a CTA over its tile, one barrier each
+constexpr int kMaxPasses = 16;      // passes of a CTA over its tile
+constexpr int kCopyPasses = Q8_CP;  // passes that one copy and its barrier bring
+constexpr int kMaxCopies = kMaxPasses / kCopyPasses;
 constexpr int kMaxHeads = 66;       // heads that a tile of 512 rows can touch (P >= 8)
 constexpr int kMaxCluster = 16;
 constexpr uint64_t kWaitLimitNs = 1000000000ull;
@@ -73,15 +87,14 @@ __device__ __forceinline__ void unpack_word(uint32_t u, float* out) {
 
 // Byte offsets of the dynamic shared memory of a CTA.
 struct Layout {
-    int scale, conv_x, conv_bc, rp, y, nscale, B, C, raw_bc, bytes;
+    int scale, conv_x, conv_bc, rp, y, B, C, raw_bc, bytes;
     __host__ __device__ Layout(int tile, int N, int K, int as) {
-        scale = tile * N;                       // old scales
+        scale = tile * N;                       // the old scales, later the new ones
         conv_x = scale + tile * 4;              // [K-1][tile]
         conv_bc = conv_x + (K - 1) * tile * as; // [2][K-1][N]
-        rp = conv_bc + 2 * (K - 1) * N * as;    // per row {dt*x, scale*dA, D*x, -}
-        y = rp + tile * 16;
-        nscale = y + tile * 4;
-        B = nscale + tile * 4;
+        rp = conv_bc + 2 * (K - 1) * N * as;    // per row {dt*x, scale*dA}
+        y = rp + tile * 8;                      // D*x, later y
+        B = y + tile * 4;
         C = B + N * 4;
         raw_bc = C + N * 4;                     // this step's raw B and C inputs
         bytes = raw_bc + 2 * N * as;
@@ -99,15 +112,16 @@ __device__ __forceinline__ float reduce_two(float v0, float v1, bool upper, Op o
 }
 
 template <typename AT, int N, bool NORM>
-__global__ void __launch_bounds__(kThreads, 2) q8_update_kernel(const Q8UpdateArgs a) {
+__global__ void __launch_bounds__(kThreads, Q8_MINB) q8_update_kernel(const Q8UpdateArgs a) {
     constexpr int LPR = N / 16;
     constexpr int RPP = kThreads / LPR;              // rows a CTA covers once
     constexpr int PASS = RPP * kRowsPerThread;       // rows of one pass
     constexpr int CW = 4 / sizeof(AT);               // channels per 32-bit word
     constexpr int AS = sizeof(AT);
+    constexpr int kPre = (Q8_TILE + 2 * N) / CW >= 3 * kThreads ? 3 : ((Q8_TILE + 2 * N) / CW >= 2 * kThreads ? 2 : 1);
 
     extern __shared__ __align__(128) uint8_t s_dyn[];
-    __shared__ __align__(8) uint64_t s_bar[kMaxPasses + 1];
+    __shared__ __align__(8) uint64_t s_bar[kMaxCopies + 1];
     __shared__ float s_dt[kMaxHeads], s_dA[kMaxHeads], s_D[kMaxHeads];
     __shared__ int s_fail;
     __shared__ float s_red[kWarps], s_parts[kMaxCluster], s_rstd;
@@ -128,12 +142,11 @@ __global__ void __launch_bounds__(kThreads, 2) q8_update_kernel(const Q8UpdateAr
     const int64_t cC = cB + static_cast<int64_t>(a.G) * N;
     const Layout L(a.tile_rows, N, K, AS);
     const uint8_t* s_codes = s_dyn;
-    const float* s_scale = reinterpret_cast<const float*>(s_dyn + L.scale);
+    float* s_scale = reinterpret_cast<float*>(s_dyn + L.scale);
     const AT* s_cx = reinterpret_cast<const AT*>(s_dyn + L.conv_x);
     const AT* s_cbc = reinterpret_cast<const AT*>(s_dyn + L.conv_bc);
-    float4* s_rp = reinterpret_cast<float4*>(s_dyn + L.rp);
+    float2* s_rp = reinterpret_cast<float2*>(s_dyn + L.rp);
     float* s_y = reinterpret_cast<float*>(s_dyn + L.y);
-    float* s_nscale = reinterpret_cast<float*>(s_dyn + L.nscale);
     float* s_B = reinterpret_cast<float*>(s_dyn + L.B);
     float* s_C = reinterpret_cast<float*>(s_dyn + L.C);
     uint32_t* s_rawbc = reinterpret_cast<uint32_t*>(s_dyn + L.raw_bc);
@@ -145,6 +158,38 @@ __global__ void __launch_bounds__(kThreads, 2) q8_update_kernel(const Q8UpdateAr
     const AT* xrow = static_cast<const AT*>(a.xBC) + b * a.xBC_stride;
     const AT* zrow = a.z ? static_cast<const AT*>(a.z) + b * a.z_stride : nullptr;
     AT* yrow = static_cast<AT*>(a.y) + b * a.y_stride;
+    // ---- what does not depend on the slot is loaded before the slot is read:
+    // its latency hides behind the slot's and the copies'
+    const int n_words = (nrows + 2 * N) / CW;  // conv words: x of the tile, then B and C
+    const int nx = nrows / CW;
+    const AT* w = static_cast<const AT*>(a.conv_w);
+    const AT* bias = static_cast<const AT*>(a.conv_b);
+    auto word_channel = [&](int q) -> int64_t {
+        if (q < nx) return r0 + q * CW;
+        const int j = (q - nx) * CW;
+        return j < N ? cB + j : cC + (j - N);
+    };
+    uint32_t raw_in[kPre], bias_in[kPre];
+    uint4 w_in[kPre];
+#pragma unroll
+    for (int i = 0; i < kPre; ++i) {
+        const int q = i * kThreads + tid;
+        raw_in[i] = bias_in[i] = 0;
+        w_in[i] = make_uint4(0, 0, 0, 0);
+        if (q < n_words) {
+            const int64_t c0 = word_channel(q);
+            raw_in[i] = *reinterpret_cast<const uint32_t*>(xrow + c0);
+            if (bias) bias_in[i] = __ldg(reinterpret_cast<const uint32_t*>(bias + c0));
+            if (K == 4) w_in[i] = __ldg(reinterpret_cast<const uint4*>(w + c0 * 4));
+        }
+    }
+    float hs_dt = 0.f, hs_bias = 0.f, hs_alog = 0.f, hs_D = 0.f;
+    if (tid < n_heads) {
+        hs_dt = to_f32(static_cast<const AT*>(a.dt)[b * a.dt_stride + h_first + tid]);
+        hs_bias = a.dt_bias[h_first + tid];
+        hs_alog = a.A_log[h_first + tid];
+        hs_D = a.D[h_first + tid];
+    }
     const int32_t slot = a.slot_idx[b];
     // skipped rows are skipped by the whole cluster
     if (slot < 0) {
@@ -159,11 +204,14 @@ __global__ void __launch_bounds__(kThreads, 2) q8_update_kernel(const Q8UpdateAr
     int8_t* tile = a.ssm + row_base * N;
     float* scales = a.scale + row_base;
     AT* conv0 = static_cast<AT*>(a.conv) + static_cast<int64_t>(slot) * (K - 1) * cd;
-    uint64_t* bar_conv = &s_bar[kMaxPasses];
+    uint64_t* bar_conv = &s_bar[kMaxCopies];
+    constexpr int COPY = PASS * kCopyPasses;  // rows of one copy
     const int passes = (nrows + PASS - 1) / PASS;
+    const int copies = (nrows + COPY - 1) / COPY;
     if (tid == 0) {
         s_fail = 0;
-        for (int c = 0; c <= kMaxPasses; ++c) mbar_init(&s_bar[c], 1);
+        for (int c = 0; c < copies; ++c) mbar_init(&s_bar[c], 1);
+        mbar_init(bar_conv, 1);
         fence_mbar_init();
         mbar_arrive_expect_tx(bar_conv, static_cast<uint32_t>((K - 1) * (nrows + 2 * N) * AS + nrows * 4));
         bulk_g2s(s_dyn + L.scale, scales, nrows * 4, bar_conv);
@@ -172,51 +220,36 @@ __global__ void __launch_bounds__(kThreads, 2) q8_update_kernel(const Q8UpdateAr
             bulk_g2s(s_dyn + L.conv_bc + k * N * AS, conv0 + k * cd + cB, N * AS, bar_conv);
             bulk_g2s(s_dyn + L.conv_bc + (K - 1 + k) * N * AS, conv0 + k * cd + cC, N * AS, bar_conv);
         }
-        for (int c = 0; c < passes; ++c) {
-            const int rows = min(PASS, nrows - c * PASS);
+        for (int c = 0; c < copies; ++c) {
+            const int rows = min(COPY, nrows - c * COPY);
             mbar_arrive_expect_tx(&s_bar[c], rows * N);
-            bulk_g2s(s_dyn + c * PASS * N, tile + static_cast<int64_t>(c) * PASS * N, rows * N, &s_bar[c]);
+            bulk_g2s(s_dyn + c * COPY * N, tile + static_cast<int64_t>(c) * COPY * N, rows * N, &s_bar[c]);
         }
     }
     asm volatile("griddepcontrol.launch_dependents;\n" ::: "memory");
     if (tid < n_heads) {
-        const int h = h_first + tid;
-        const float dt = softplus_f32(to_f32(static_cast<const AT*>(a.dt)[b * a.dt_stride + h]) + a.dt_bias[h]);
+        const float dt = softplus_f32(hs_dt + hs_bias);
         s_dt[tid] = dt;
-        s_dA[tid] = expf(dt * -expf(a.A_log[h]));
-        s_D[tid] = a.D[h];
+        s_dA[tid] = expf(dt * -expf(hs_alog));
+        s_D[tid] = hs_D;
     }
     __syncthreads();
 
     // ---- conv: one word of channels at a time, x of the tile, then B and C
     {
-        const AT* w = static_cast<const AT*>(a.conv_w);
-        const AT* bias = static_cast<const AT*>(a.conv_b);
-        const int nx = nrows / CW;
-        for (int q = tid; q < nx + 2 * N / CW; q += kThreads) {
+        auto conv_word = [&](int q, uint32_t raw, uint32_t bias_w, uint4 wv) {
             const bool is_x = q < nx;
             const int j = is_x ? q * CW : (q - nx) * CW;  // channel within the segment(s)
             const int seg = j / N;                        // (B, C) 0 or 1
-            const int64_t c0 = is_x ? r0 + j : (seg ? cC : cB) + (j - seg * N);
+            const int64_t c0 = word_channel(q);
             const AT* rows = is_x ? s_cx + j : s_cbc + seg * (K - 1) * N + (j - seg * N);
             const int pitch = is_x ? a.tile_rows : N;
-            const uint32_t raw = *reinterpret_cast<const uint32_t*>(xrow + c0);
-            float out[CW], xv[CW];
-            unpack_word<AT>(bias ? __ldg(reinterpret_cast<const uint32_t*>(bias + c0)) : 0u, out);
-            unpack_word<AT>(raw, xv);
-            float w4[CW * 4];
+            float out[CW];
+            unpack_word<AT>(bias_w, out);
             if (K == 4) {  // the CW x 4 weights are one 16-byte vector
-                float t[Vec16<AT>::n];
-                unpack16<AT>(__ldg(reinterpret_cast<const uint4*>(w + c0 * 4)), t);
-#pragma unroll
-                for (int i = 0; i < CW * 4; ++i) w4[i] = t[i];
-            }
-            if (!mbar_wait_bounded(bar_conv, 0, kWaitLimitNs)) {
-                record_error(a.error, M2_ERR_TIMEOUT);
-                s_fail = 1;
-                break;
-            }
-            if (K == 4) {
+                float w4[Vec16<AT>::n], xv[CW];
+                unpack16<AT>(wv, w4);
+                unpack_word<AT>(raw, xv);
 #pragma unroll
                 for (int k = 0; k < 3; ++k) {
                     float rv[CW];
@@ -245,14 +278,32 @@ __global__ void __launch_bounds__(kThreads, 2) q8_update_kernel(const Q8UpdateAr
                 const int hl = (rr0 + j) / P;  // CW channels lie in one head
                 const float dtv = s_dt[hl], dAv = s_dA[hl], Dv = s_D[hl];
 #pragma unroll
-                for (int e = 0; e < CW; ++e)
-                    s_rp[j + e] = make_float4(dtv * out[e], s_scale[j + e] * dAv, Dv * out[e], 0.f);
+                for (int e = 0; e < CW; ++e) {
+                    s_rp[j + e] = make_float2(dtv * out[e], s_scale[j + e] * dAv);
+                    s_y[j + e] = Dv * out[e];
+                }
             } else {
                 float* dst = (seg ? s_C : s_B) + (j - seg * N);
 #pragma unroll
                 for (int e = 0; e < CW; ++e) dst[e] = out[e];
                 s_rawbc[j / CW] = raw;
             }
+        };
+        if (mbar_wait_bounded(bar_conv, 0, kWaitLimitNs)) {
+#pragma unroll
+            for (int i = 0; i < kPre; ++i) {
+                const int q = i * kThreads + tid;
+                if (q < n_words) conv_word(q, raw_in[i], bias_in[i], w_in[i]);
+            }
+            for (int q = kPre * kThreads + tid; q < n_words; q += kThreads) {
+                const int64_t c0 = word_channel(q);
+                conv_word(q, *reinterpret_cast<const uint32_t*>(xrow + c0),
+                          bias ? __ldg(reinterpret_cast<const uint32_t*>(bias + c0)) : 0u,
+                          K == 4 ? __ldg(reinterpret_cast<const uint4*>(w + c0 * 4)) : make_uint4(0, 0, 0, 0));
+            }
+        } else {
+            record_error(a.error, M2_ERR_TIMEOUT);
+            s_fail = 1;
         }
         cluster_arrive_relaxed();  // this CTA has read the group's B/C conv rows
     }
@@ -269,9 +320,14 @@ __global__ void __launch_bounds__(kThreads, 2) q8_update_kernel(const Q8UpdateAr
         B2[e] = *reinterpret_cast<const float2*>(s_B + l * 16 + 2 * e);
         C2[e] = *reinterpret_cast<const float2*>(s_C + l * 16 + 2 * e);
     }
+    // row (c * 2 + i) * RPP + tid / LPR of the tile is codes ((c * 2 + i) * kThreads + tid) * 16 .. + 15
+    const float2* rps = s_rp + tid / LPR;
+    const uint8_t* codes = s_codes + tid * 16;
+    int8_t* out = tile + tid * 16;
+    const int end = nrows * N - tid * 16;  // codes of this thread's rows that exist lie below
 #pragma unroll 1
-    for (int c = 0; c < passes && ok; ++c) {
-        if (!mbar_wait_bounded(&s_bar[c], 0, kWaitLimitNs)) {
+    for (int c = 0; c < passes; ++c) {
+        if (c % kCopyPasses == 0 && !mbar_wait_bounded(&s_bar[c / kCopyPasses], 0, kWaitLimitNs)) {
             record_error(a.error, M2_ERR_TIMEOUT);
             ok = false;
             break;
@@ -280,9 +336,8 @@ __global__ void __launch_bounds__(kThreads, 2) q8_update_kernel(const Q8UpdateAr
         float sum[kRowsPerThread], big[kRowsPerThread];
 #pragma unroll
         for (int i = 0; i < kRowsPerThread; ++i) {
-            const int row = c * PASS + i * RPP + tid / LPR;  // < tile_rows
-            const float4 rp = s_rp[row];
-            const uint4 w = *reinterpret_cast<const uint4*>(s_codes + row * N + l * 16);
+            const float2 rp = rps[(c * kRowsPerThread + i) * RPP];
+            const uint4 w = *reinterpret_cast<const uint4*>(codes + (c * kRowsPerThread + i) * (kThreads * 16));
             const uint32_t words[4] = {w.x, w.y, w.z, w.w};
             const float2 dtx = make_float2(rp.x, rp.x), k2 = make_float2(rp.y, rp.y);
             float2 acc = make_float2(0.f, 0.f);
@@ -295,8 +350,8 @@ __global__ void __launch_bounds__(kThreads, 2) q8_update_kernel(const Q8UpdateAr
                 hi = __ffma2_rn(hi, k2, __fmul2_rn(dtx, B2[2 * q + 1]));
                 acc = __ffma2_rn(lo, C2[2 * q], acc);
                 acc = __ffma2_rn(hi, C2[2 * q + 1], acc);
-                m = max_nan(max_nan(m, fabsf(lo.x)), fabsf(lo.y));
-                m = max_nan(max_nan(m, fabsf(hi.x)), fabsf(hi.y));
+                m = max_abs(m, lo.x, lo.y);
+                m = max_abs(m, hi.x, hi.y);
                 S[i][2 * q] = lo;
                 S[i][2 * q + 1] = hi;
             }
@@ -306,39 +361,36 @@ __global__ void __launch_bounds__(kThreads, 2) q8_update_kernel(const Q8UpdateAr
         const float ysum = reduce_two<LPR>(sum[0], sum[1], upper, [](float u, float v) { return u + v; });
         const float amax = reduce_two<LPR>(big[0], big[1], upper, [](float u, float v) { return max_nan(u, v); });
         float scale, inv;
-        q8_scale(amax, scale, inv);
+        q8_scale_fast(amax, scale, inv);
         if (l % (LPR / 2) == 0) {
-            const int row = c * PASS + (upper ? RPP : 0) + tid / LPR;
-            if (row < nrows) {
-                s_y[row] = ysum + s_rp[row].z;
-                s_nscale[row] = scale;
-            }
+            const int row = (c * kRowsPerThread + (upper ? 1 : 0)) * RPP + tid / LPR;  // < tile_rows
+            s_y[row] += ysum;
+            s_scale[row] = scale;
         }
         float inv_of[kRowsPerThread];
         inv_of[0] = __shfl_sync(0xffffffffu, inv, lane & ~(LPR / 2));
         inv_of[1] = __shfl_sync(0xffffffffu, inv, lane | (LPR / 2));
 #pragma unroll
         for (int i = 0; i < kRowsPerThread; ++i) {
-            const int row = c * PASS + i * RPP + tid / LPR;
             const float2 iv = make_float2(inv_of[i], inv_of[i]), mg = make_float2(kQ8Magic, kQ8Magic);
-            uint32_t out[4];
+            uint32_t o[4];
 #pragma unroll
             for (int q = 0; q < 4; ++q) {
                 const float2 lo = __ffma2_rn(S[i][2 * q], iv, mg), hi = __ffma2_rn(S[i][2 * q + 1], iv, mg);
-                out[q] = q8_pack(lo.x, lo.y, hi.x, hi.y);
+                o[q] = q8_pack(lo.x, lo.y, hi.x, hi.y);
             }
-            if (row < nrows)
-                st_stream(tile + static_cast<int64_t>(row) * N + l * 16, make_uint4(out[0], out[1], out[2], out[3]));
+            const int at = (c * kRowsPerThread + i) * (kThreads * 16);
+            if (at < end) st_stream(out + at, make_uint4(o[0], o[1], o[2], o[3]));
         }
     }
     if (!ok) {  // let this CTA's copies land before its shared memory goes
-        for (int c = 0; c < passes; ++c) mbar_wait_bounded(&s_bar[c], 0, kWaitLimitNs);
+        for (int c = 0; c < copies; ++c) mbar_wait_bounded(&s_bar[c], 0, kWaitLimitNs);
         mbar_wait_bounded(bar_conv, 0, kWaitLimitNs);
     }
     __syncthreads();
 
     if (ok) {
-        for (int i = tid; i < nrows; i += kThreads) scales[i] = s_nscale[i];
+        for (int i = tid; i < nrows; i += kThreads) scales[i] = s_scale[i];
     }
     if constexpr (!NORM) {
         if (ok) {
@@ -456,7 +508,7 @@ m2_status q8_shape_supported(int H, int P, int N, int G) {
 
 cudaError_t launch_q8_update(Q8UpdateArgs a, cudaStream_t stream) {
     const int group_rows = a.H / a.G * a.P;
-    int tile = std::min(256, max_tile(a.N));
+    int tile = std::min(Q8_TILE, max_tile(a.N));
     if (group_rows < tile) tile = (group_rows + pass_rows(a.N) - 1) / pass_rows(a.N) * pass_rows(a.N);
     while ((group_rows + tile - 1) / tile > kMaxCluster) tile *= 2;
     a.tile_rows = tile;
