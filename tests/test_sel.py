@@ -219,6 +219,25 @@ def test_scan_lengths(lengths, act):
 
 
 @pytest.mark.gpu
+@pytest.mark.parametrize("shape", [m2.SelShape(64, 16, 1, 4, F32, BF16), m2.SelShape(40, 8, 1, 4, F32, F32), m2.SelShape(48, 32, 2, 4, BF16, BF16),
+                                   m2.SelShape(24, 64, 1, 4, F32, F32), m2.SelShape(16, 128, 2, 4, F32, BF16)], ids=str)
+def test_scan_in_segments(shape):
+    """One long prompt of few channels is cut into segments; beside it an empty
+    one, ones shorter than a segment or a tile, a padding row and a bad slot."""
+    lengths = [1200, 0, 3, 65, 300, 1, 20, 9]
+    layer = Layer(shape, sum(lengths))
+    cache = cache_of(shape, 9)
+    slots = ints(4, 2, 0, 1, 8, 3, -1, 9)
+    init = torch.tensor([1, 1, 0, 1, 1, 1, 0, 1], dtype=torch.uint8, device="cuda")
+    before = cache.ssm.clone()
+    y = torch.full((sum(lengths), shape.D), 9.0, dtype=TYPES[shape.act_dtype], device="cuda")
+    m2.sel_scan(cache, layer.params, layer.x, layer.dt, layer.B, layer.C, offsets(lengths), slots, max_seqlen=1200, z=layer.z,
+                has_initial_state=init, y=y)
+    assert (y[-9:] == 9).all() and cache.device_error() == m2.M2_ERR_BAD_SLOT
+    check_scan(layer, cache, lengths[:-1], slots, init, y, before)
+
+
+@pytest.mark.gpu
 @pytest.mark.parametrize("D", [512, 4096])
 def test_scan_of_many_channels(D):
     """Enough channels for every way of spreading a channel's states over lanes."""
