@@ -618,34 +618,36 @@ def _need(ok: bool, what: str) -> None:
         raise ValueError(what)
 
 
+# The checks below run on every call of a decode step: a failed one is put into
+# words only once it has failed.
+
 def _rows(t: Optional[torch.Tensor], name: str, rows: int, width: int, dtype: torch.dtype,
           device: torch.device) -> int:
     """Checks a [rows, width] tensor (unit stride inside a row) and returns its row stride."""
     if t is None:
         return 0
-    _need(t.dtype == dtype, f"{name} must be {dtype}, not {t.dtype}")
-    _need(t.device == device, f"{name} is on {t.device}, the cache on {device}")
-    _need(t.dim() == 2 and t.shape[0] == rows and t.shape[1] == width,
-          f"{name} must be [{rows}, {width}], not {list(t.shape)}")
-    _need(t.stride(1) == 1, f"{name}: rows must be contiguous (unit stride in the last dimension)")
-    return t.stride(0) if rows > 1 else width
+    if t.dtype is dtype and t.shape == (rows, width) and t.device == device:
+        s0, s1 = t.stride()
+        if s1 == 1 or width == 1:
+            return s0 if rows > 1 else width
+        raise ValueError(f"{name}: rows must be contiguous (unit stride in the last dimension)")
+    raise ValueError(f"{name} must be {dtype} [{rows}, {width}] on {device}, not {t.dtype} {list(t.shape)} on {t.device}")
 
 
 def _index(t: torch.Tensor, name: str, n: int, device: torch.device) -> None:
-    _need(t.dtype == torch.int32 and t.is_contiguous() and t.numel() == n and t.device == device,
-          f"{name} must be {n} contiguous int32 on {device}")
+    if not (t.dtype is torch.int32 and t.numel() == n and t.is_contiguous() and t.device == device):
+        raise ValueError(f"{name} must be {n} contiguous int32 on {device}")
 
 
 def _param(t: Optional[torch.Tensor], name: str, n: int, dtype: torch.dtype, device: torch.device) -> None:
-    if t is not None:
-        _need(t.dtype == dtype and t.is_contiguous() and t.numel() == n and t.device == device,
-              f"{name} must be {n} contiguous {dtype} on {device}")
+    if t is not None and not (t.dtype is dtype and t.numel() == n and t.is_contiguous() and t.device == device):
+        raise ValueError(f"{name} must be {n} contiguous {dtype} on {device}")
 
 
 def _current(device: torch.device) -> None:
     """The library launches on the current device: the cache has to be there."""
-    _need(device.type == "cuda" and device.index == torch.cuda.current_device(),
-          f"the cache is on {device}, which is not the current CUDA device")
+    if device.type != "cuda" or device.index != torch.cuda.current_device():
+        raise ValueError(f"the cache is on {device}, which is not the current CUDA device")
 
 
 def _on(device: torch.device):
@@ -710,7 +712,8 @@ def _q8_copy(name: str, src, dst, src_idx: torch.Tensor, dst_idx: torch.Tensor, 
     _index(src_idx, "src_idx", n, q8.device)
     _index(dst_idx, "dst_idx", n, q8.device)
     full = dst if q8 is src else src
-    _need(full.ssm is None or full.ssm.device == q8.device, "the two caches are on different devices")
+    if full.ssm is not None and full.ssm.device != q8.device:
+        raise ValueError("the two caches are on different devices")
     _current(q8.device)
     _check(getattr(lib(), name)(ctypes.byref(src.c), ctypes.byref(dst.c), n, src_idx.data_ptr(), dst_idx.data_ptr(),
                                 _stream_ptr() if stream is None else stream), name)
@@ -720,7 +723,8 @@ def q8_store(src: Cache, dst: Q8Cache, src_idx: torch.Tensor, dst_idx: torch.Ten
              stream: Optional[int] = None) -> None:
     """Quantises the states of ``src`` slots ``src_idx`` into ``dst`` slots
     ``dst_idx`` (m2_q8_store); the conv rows are copied."""
-    _need(isinstance(src, Cache) and isinstance(dst, Q8Cache), "q8_store copies a Cache into a Q8Cache")
+    if not (isinstance(src, Cache) and isinstance(dst, Q8Cache)):
+        raise ValueError("q8_store copies a Cache into a Q8Cache")
     _q8_copy("m2_q8_store", src, dst, src_idx, dst_idx, stream)
 
 
@@ -728,7 +732,8 @@ def q8_load(src: Q8Cache, dst: Cache, src_idx: torch.Tensor, dst_idx: torch.Tens
             stream: Optional[int] = None) -> None:
     """Reads ``src`` slots ``src_idx`` (which may repeat) back into ``dst`` slots
     ``dst_idx`` (m2_q8_load)."""
-    _need(isinstance(src, Q8Cache) and isinstance(dst, Cache), "q8_load copies a Q8Cache into a Cache")
+    if not (isinstance(src, Q8Cache) and isinstance(dst, Cache)):
+        raise ValueError("q8_load copies a Q8Cache into a Cache")
     _q8_copy("m2_q8_load", src, dst, src_idx, dst_idx, stream)
 
 
@@ -743,25 +748,28 @@ def q8_state_update(cache: Q8Cache, ssm: SSMParams, conv: ConvParams, xBC: torch
     batch, hp = xBC.shape[0], sh.H * sh.P
     if y is None:
         y = torch.empty((batch, hp), dtype=act, device=dev)
-    strides = [_rows(t, name, batch, width, act, dev)
-               for t, name, width in ((xBC, "xBC", sh.conv_dim), (dt, "dt", sh.H), (z, "z", hp), (y, "y", hp))]
+    cd = sh.conv_dim
+    xs, ds = _rows(xBC, "xBC", batch, cd, act, dev), _rows(dt, "dt", batch, sh.H, act, dev)
+    zs, ys = _rows(z, "z", batch, hp, act, dev), _rows(y, "y", batch, hp, act, dev)
     _index(slot_idx, "slot_idx", batch, dev)
-    for t, name in ((ssm.A_log, "A_log"), (ssm.dt_bias, "dt_bias"), (ssm.D, "D")):
-        _param(t, name, sh.H, torch.float32, dev)
-    _param(conv.weight, "conv weight", sh.conv_dim * sh.K, act, dev)
-    _param(conv.bias, "conv bias", sh.conv_dim, act, dev)
+    _param(ssm.A_log, "A_log", sh.H, torch.float32, dev)
+    _param(ssm.dt_bias, "dt_bias", sh.H, torch.float32, dev)
+    _param(ssm.D, "D", sh.H, torch.float32, dev)
+    _param(conv.weight, "conv weight", cd * sh.K, act, dev)
+    _param(conv.bias, "conv bias", cd, act, dev)
     if norm is not None:
         _param(norm.weight, "norm weight", hp, act, dev)
     _current(dev)
-    sp, cp = ssm.c(), conv.c()
-    rest = [batch, xBC.data_ptr(), strides[0], dt.data_ptr(), strides[1], _ptr(z), strides[2], y.data_ptr(), strides[3],
-            slot_idx.data_ptr(), _stream_ptr() if stream is None else stream]
+    sp = m2_ssm_params(ssm.A_log.data_ptr(), ssm.dt_bias.data_ptr(), ssm.D.data_ptr())
+    cp = m2_conv_params(conv.weight.data_ptr(), _ptr(conv.bias), conv.activation)
+    rest = (batch, xBC.data_ptr(), xs, dt.data_ptr(), ds, _ptr(z), zs, y.data_ptr(), ys, slot_idx.data_ptr(),
+            _stream_ptr() if stream is None else stream)
     if norm is not None:
         npar = norm.c()
-        _check(lib().m2_q8_state_update_norm(ctypes.byref(cache.c), ctypes.byref(sp), ctypes.byref(cp),
+        _check(lib().m2_q8_state_update_norm(ctypes.byref(cache._c), ctypes.byref(sp), ctypes.byref(cp),
                                              ctypes.byref(npar), *rest), "m2_q8_state_update_norm")
     else:
-        _check(lib().m2_q8_state_update(ctypes.byref(cache.c), ctypes.byref(sp), ctypes.byref(cp), *rest),
+        _check(lib().m2_q8_state_update(ctypes.byref(cache._c), ctypes.byref(sp), ctypes.byref(cp), *rest),
                "m2_q8_state_update")
     return y
 
@@ -847,20 +855,28 @@ class SelParams:
         return m2_sel_params(self.A_log.data_ptr(), self.dt_bias.data_ptr(), self.D.data_ptr())
 
 
-def _sel_rows(cache: SelCache, x, dt, B, C, z, y) -> list:
+def _sel_rows(cache: SelCache, x, dt, B, C, z, y) -> tuple:
     """Pointers and row strides of a per-channel call's tensors, checked."""
     sh, dev = cache.shape, cache.device
     act = torch_dtype(sh.act_dtype)
-    T, gn = x.shape[0], sh.G * sh.N
-    out = []
-    for t, name, width in ((x, "x", sh.D), (dt, "dt", sh.D), (B, "B", gn), (C, "C", gn), (z, "z", sh.D), (y, "y", sh.D)):
-        if t is not None and t.dim() == 3 and name in "BC":  # [T, G, N]: a row is its G*N values
-            _need(t.shape[1:] == (sh.G, sh.N) and t.stride(2) == 1 and (sh.G == 1 or t.stride(1) == sh.N),
-                  f"{name} must be [{T}, {sh.G}, {sh.N}] with contiguous rows, not {list(t.shape)}")
-            t = t.as_strided((t.shape[0], gn), (t.stride(0), 1))
-        stride = _rows(t, name, T, width, act, dev)
-        out += [_ptr(t), stride]
-    return out
+    T = x.shape[0]
+    D = sh.D
+    return (x.data_ptr(), _rows(x, "x", T, D, act, dev), dt.data_ptr(), _rows(dt, "dt", T, D, act, dev),
+            B.data_ptr(), _sel_bc(B, "B", T, sh, act, dev), C.data_ptr(), _sel_bc(C, "C", T, sh, act, dev),
+            _ptr(z), _rows(z, "z", T, D, act, dev), y.data_ptr(), _rows(y, "y", T, D, act, dev))
+
+
+def _sel_bc(t: torch.Tensor, name: str, T: int, sh: SelShape, act: torch.dtype, dev: torch.device) -> int:
+    """Checks B or C, [T, G*N] or [T, G, N] with a row's values side by side, and returns its row stride."""
+    G, N = sh.G, sh.N
+    if t.dim() != 3:
+        return _rows(t, name, T, G * N, act, dev)
+    if t.dtype is act and t.shape == (T, G, N) and t.device == dev:
+        s0, s1, s2 = t.stride()
+        if s2 == 1 and (G == 1 or s1 == N):
+            return s0 if T > 1 else G * N
+    raise ValueError(f"{name} must be {act} [{T}, {G}, {N}] with contiguous rows on {dev}, not {t.dtype} {list(t.shape)} "
+                     f"with strides {list(t.stride())} on {t.device}")
 
 
 def sel_state_update(cache: SelCache, params: SelParams, x: torch.Tensor, dt: torch.Tensor, B: torch.Tensor,
@@ -875,7 +891,7 @@ def sel_state_update(cache: SelCache, params: SelParams, x: torch.Tensor, dt: to
     _index(slot_idx, "slot_idx", x.shape[0], cache.device)
     sp = params.c(cache.shape, cache.device)
     _current(cache.device)
-    _check(lib().m2_sel_state_update(ctypes.byref(cache.c), ctypes.byref(sp), x.shape[0], *rows, slot_idx.data_ptr(),
+    _check(lib().m2_sel_state_update(ctypes.byref(cache._c), ctypes.byref(sp), x.shape[0], *rows, slot_idx.data_ptr(),
                                      _stream_ptr() if stream is None else stream), "m2_sel_state_update")
     return y
 
@@ -901,7 +917,7 @@ def sel_scan(cache: SelCache, params: SelParams, x: torch.Tensor, dt: torch.Tens
         _need(has_initial_state.dtype in (torch.uint8, torch.bool), "has_initial_state must be uint8 or bool")
     sp = params.c(cache.shape, dev)
     _current(dev)
-    _check(lib().m2_sel_scan(ctypes.byref(cache.c), ctypes.byref(sp), nseq, cu_seqlens.data_ptr(), x.shape[0],
+    _check(lib().m2_sel_scan(ctypes.byref(cache._c), ctypes.byref(sp), nseq, cu_seqlens.data_ptr(), x.shape[0],
                              x.shape[0] if max_seqlen is None else max_seqlen, *rows, slot_idx.data_ptr(),
                              _ptr(has_initial_state), _stream_ptr() if stream is None else stream), "m2_sel_scan")
     return y
