@@ -48,6 +48,21 @@ cudaError_t launch_sel_update(const SelArgs& a, cudaStream_t stream);
 
 constexpr float kLog2E = 1.4426950408889634f;
 
+// How exact the factors are goes by the activations' type. fp32 ones get the
+// library's expf and log1pf on dt * A itself, within an ulp or two each; for
+// 16-bit ones, whose own rounding is 2^-9, the special-function unit's 2^x
+// (2^-22) of dt * (A log2 e) and the softplus below do.
+template <typename AT>
+struct Decay {
+    static constexpr bool kExact = sizeof(AT) == 4;
+    // what a state keeps of its A, and the decay over dt by it
+    __device__ static __forceinline__ float factor(float A_log) {
+        return kExact ? -expf(A_log) : -kLog2E * ex2_approx(A_log * kLog2E);
+    }
+    __device__ static __forceinline__ float over(float x) { return kExact ? expf(x) : ex2_approx(x); }  // x = dt * factor
+    __device__ static __forceinline__ float2 softplus(float2 v);
+};
+
 // softplus of a pair: max(v, 0) + log1p(u), u = exp(-|v|) in (0, 1], with
 // log1p(u) = u (1 + u r(u)), r the minimax polynomial of degree 7 on [0, 1]
 // (fitted by exchange for the relative error: 3.3e-8, 1.6e-7 with its fp32
@@ -67,6 +82,11 @@ __device__ __forceinline__ float2 softplus2_fast(float2 v) {
     p = __ffma2_rn(p, u, both(-0.49999648f));
     p = __ffma2_rn(p, u, both(1.f));
     return __ffma2_rn(p, u, make_float2(fmaxf(v.x, 0.f), fmaxf(v.y, 0.f)));
+}
+
+template <typename AT>
+__device__ __forceinline__ float2 Decay<AT>::softplus(float2 v) {
+    return kExact ? make_float2(softplus_f32(v.x), softplus_f32(v.y)) : softplus2_fast(v);
 }
 
 }  // namespace m2

@@ -11,7 +11,7 @@
 //    and leave both in shared memory, B and C beside them as floats; and they
 //    finish the tile that the scan has done: D x is added, y gated and stored
 //    (16-bit outputs with the tanh form of the SiLU, as the prefill conv);
-//  * the scan (128 threads) runs h = h * 2^(dt * A log2 e) + (dt x) B and sums
+//  * the scan (128 threads) runs h = h * exp(dt A) + (dt x) B and sums
 //    h * C, four tokens at a time: shared memory holds every channel's (and
 //    every state's) tokens side by side, so that a lane reads four tokens at
 //    once and the packed f32x2 arithmetic takes pairs of tokens. The sums of
@@ -69,6 +69,7 @@ __device__ __forceinline__ float ld_cluster_f32(const float* local, uint32_t ran
 
 template <typename AT, int LPC, int SPL>
 struct Scan {
+    using Factors = Decay<AT>;
     static constexpr int N = LPC * SPL;
     static constexpr int CB = kScan / LPC;
     static constexpr int VEC = Vec16<AT>::n;
@@ -120,7 +121,7 @@ __device__ __forceinline__ void put_sums(float* y, float2 y01, float2 y23, int l
 // The tokens of one tile for a lane's states s * LPC + l of channel lc. Y: y is
 // wanted; otherwise the sum of dt is.
 template <bool Y, int SPL, int LPC, typename K>
-__device__ __forceinline__ void scan_tile(typename K::Buffer& buf, const float (&A2)[SPL], float (&h)[SPL], float& sum_dt, int lc, int l,
+__device__ __forceinline__ void scan_tile(typename K::Buffer& buf, const float (&A)[SPL], float (&h)[SPL], float& sum_dt, int lc, int l,
                                           int lane) {
     constexpr int TT = K::TT, P = K::P;
     const float* d_of = buf.d[lc];
@@ -153,13 +154,13 @@ __device__ __forceinline__ void scan_tile(typename K::Buffer& buf, const float (
         float2 y01, y23;
 #pragma unroll
         for (int s = 0; s < SPL; ++s) {
-            const float2 a2 = make_float2(A2[s], A2[s]);
+            const float2 a2 = make_float2(A[s], A[s]);
             const float2 x01 = __fmul2_rn(d01, a2), x23 = __fmul2_rn(d23, a2);
             const float2 v01 = __fmul2_rn(u01, make_float2(b[s].x, b[s].y)), v23 = __fmul2_rn(u23, make_float2(b[s].z, b[s].w));
-            const float h0 = fmaf(h[s], ex2_approx(x01.x), v01.x);
-            const float h1 = fmaf(h0, ex2_approx(x01.y), v01.y);
-            const float h2 = fmaf(h1, ex2_approx(x23.x), v23.x);
-            h[s] = fmaf(h2, ex2_approx(x23.y), v23.y);
+            const float h0 = fmaf(h[s], K::Factors::over(x01.x), v01.x);
+            const float h1 = fmaf(h0, K::Factors::over(x01.y), v01.y);
+            const float h2 = fmaf(h1, K::Factors::over(x23.x), v23.x);
+            h[s] = fmaf(h2, K::Factors::over(x23.y), v23.y);
             if constexpr (Y) {
                 const float2 c01 = make_float2(c[s].x, c[s].y), c23 = make_float2(c[s].z, c[s].w);
                 y01 = s == 0 ? __fmul2_rn(make_float2(h0, h1), c01) : __ffma2_rn(make_float2(h0, h1), c01, y01);
@@ -223,10 +224,10 @@ __global__ void __launch_bounds__(kThreads, kMinBlocks) sel_scan_kernel(const Se
         const bool live = lc < nch;
         const int64_t ch = c0 + (live ? lc : 0);
         ST* state = static_cast<ST*>(a.ssm) + (static_cast<int64_t>(slot) * a.D + ch) * N + l;  // states s * LPC + l
-        float A2[SPL], h[SPL];
+        float A[SPL], h[SPL];  // (A: as Decay keeps it)
 #pragma unroll
         for (int s = 0; s < SPL; ++s) {
-            A2[s] = -expf(a.A_log[ch * N + s * LPC + l]) * kLog2E;
+            A[s] = K::Factors::factor(a.A_log[ch * N + s * LPC + l]);
             h[s] = 0.f;
         }
         float sum_dt = 0.f;
@@ -234,7 +235,7 @@ __global__ void __launch_bounds__(kThreads, kMinBlocks) sel_scan_kernel(const Se
         if (ahead) {
             for (int i = first; i < last; ++i, ++q) {
                 bar_sync(kFull + (q & 1));
-                scan_tile<false, SPL, LPC, K>(sm.buf[q & 1], A2, h, sum_dt, lc, l, tid & 31);
+                scan_tile<false, SPL, LPC, K>(sm.buf[q & 1], A, h, sum_dt, lc, l, tid & 31);
                 bar_arrive(kDone + (q & 1));
             }
 #pragma unroll
@@ -253,13 +254,13 @@ __global__ void __launch_bounds__(kThreads, kMinBlocks) sel_scan_kernel(const Se
                 const float dt = ld_cluster_f32(&sm.end_dt[lc], r);
 #pragma unroll
                 for (int s = 0; s < SPL; ++s)
-                    h[s] = fmaf(h[s], ex2_approx(dt * A2[s]), ld_cluster_f32(&sm.end_h[lc][s * LPC + l], r));
+                    h[s] = fmaf(h[s], K::Factors::over(dt * A[s]), ld_cluster_f32(&sm.end_h[lc][s * LPC + l], r));
             }
             cluster_arrive();  // done with the others' shared memory
         }
         for (int i = first; i < last; ++i, ++q) {
             bar_sync(kFull + (q & 1));
-            scan_tile<true, SPL, LPC, K>(sm.buf[q & 1], A2, h, sum_dt, lc, l, tid & 31);
+            scan_tile<true, SPL, LPC, K>(sm.buf[q & 1], A, h, sum_dt, lc, l, tid & 31);
             bar_arrive(kDone + (q & 1));
         }
         if (live && first < last && last == all_tiles) {
@@ -323,7 +324,7 @@ __global__ void __launch_bounds__(kThreads, kMinBlocks) sel_scan_kernel(const Se
 #pragma unroll
                 for (int e = 0; e < VEC; e += 2) {
                     const float2 bias = *reinterpret_cast<const float2*>(&sm.bias[vc + e]);
-                    float2 d = softplus2_fast(__fadd2_rn(make_float2(dv[e], dv[e + 1]), bias));
+                    float2 d = K::Factors::softplus(__fadd2_rn(make_float2(dv[e], dv[e + 1]), bias));
                     if (!real) d = make_float2(0.f, 0.f);
                     const float2 u = __fmul2_rn(d, make_float2(xv[e], xv[e + 1]));
                     buf.d[vc + e][at] = d.x;

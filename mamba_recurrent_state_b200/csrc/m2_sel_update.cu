@@ -112,7 +112,7 @@ __global__ void __launch_bounds__(kThreads, kMinBlocks) sel_update_kernel(const 
 
     // ======== the update
     const int l = tid % LPC;
-    float A2[kVectors][EPV], bias[kVectors], skip[kVectors];
+    float A[kVectors][EPV], bias[kVectors], skip[kVectors];
 #pragma unroll
     for (int u = 0; u < kVectors; ++u) {
         const int c = min(tid / LPC + u * CPP, nch - 1);
@@ -121,10 +121,10 @@ __global__ void __launch_bounds__(kThreads, kMinBlocks) sel_update_kernel(const 
 #pragma unroll
         for (int e = 0; e < EPV; e += 4) {
             const float4 v = __ldg(reinterpret_cast<const float4*>(a.A_log + (c0 + c) * N + l * EPV + e));
-            A2[u][e] = -kLog2E * ex2_approx(v.x * kLog2E);
-            A2[u][e + 1] = -kLog2E * ex2_approx(v.y * kLog2E);
-            A2[u][e + 2] = -kLog2E * ex2_approx(v.z * kLog2E);
-            A2[u][e + 3] = -kLog2E * ex2_approx(v.w * kLog2E);
+            A[u][e] = Decay<AT>::factor(v.x);
+            A[u][e + 1] = Decay<AT>::factor(v.y);
+            A[u][e + 2] = Decay<AT>::factor(v.z);
+            A[u][e + 3] = Decay<AT>::factor(v.w);
         }
     }
     for (int i = 0; i < rows; ++i) {
@@ -152,14 +152,13 @@ __global__ void __launch_bounds__(kThreads, kMinBlocks) sel_update_kernel(const 
                 const int c = tid / LPC + u * CPP;
                 const int cc = min(c, nch - 1);  // (a lane past the end computes the last channel again)
                 const float xv = to_f32(st.x[cc]);
-                const float2 d2 = softplus2_fast(make_float2(to_f32(st.dt[cc]) + bias[u], 0.f));
-                const float dt = d2.x, dtx = dt * xv;
+                const float dt = Decay<AT>::softplus(make_float2(to_f32(st.dt[cc]) + bias[u], 0.f)).x, dtx = dt * xv;
                 float h[EPV];
                 unpack16<ST>(*reinterpret_cast<const uint4*>(st.state + cc * N + l * EPV), h);
                 float sum = 0.f;
 #pragma unroll
                 for (int e = 0; e < EPV; ++e) {
-                    h[e] = fmaf(h[e], ex2_approx(dt * A2[u][e]), dtx * Bv[e]);
+                    h[e] = fmaf(h[e], Decay<AT>::over(dt * A[u][e]), dtx * Bv[e]);
                     sum = fmaf(h[e], Cv[e], sum);
                 }
 #pragma unroll
