@@ -16,7 +16,7 @@ m2_status q8_shape_status(const m2_shape* s) {
     if (s->nheads <= 0 || s->head_dim <= 0 || s->d_state <= 0 || s->ngroups <= 0 || s->d_conv <= 0)
         return M2_ERR_INVALID_ARG;
     if (s->nheads % s->ngroups != 0 || !valid_dtype(s->act_dtype)) return M2_ERR_INVALID_ARG;
-    if (s->d_conv < 2 || s->d_conv > 8) return M2_ERR_UNSUPPORTED;
+    if (s->d_conv < 2 || s->d_conv > 8 || s->ngroups > 65535) return M2_ERR_UNSUPPORTED;
     // rows of a slot and channels in 32 bits, as the kernels index them
     if (static_cast<int64_t>(s->nheads) * s->head_dim > INT32_MAX || m2_conv_dim(s) > INT32_MAX) return M2_ERR_UNSUPPORTED;
     return m2::q8_shape_supported(s->nheads, s->head_dim, s->d_state, s->ngroups);

@@ -20,8 +20,8 @@ m2_status sel_shape_status(const m2_sel_shape* s) {
     if (s->d_conv < 2 || s->d_conv > 8 || !m2::sel_state_size_supported(s->d_state)) return M2_ERR_UNSUPPORTED;
     // a group's channels are taken in whole 16-byte vectors
     if (static_cast<int64_t>(s->channels / s->ngroups) * dsize(s->act_dtype) % 16 != 0) return M2_ERR_UNSUPPORTED;
-    // channel and group offsets of a row in 32 bits
-    if (s->channels > (1 << 24) || static_cast<int64_t>(s->ngroups) * s->d_state > (1 << 24)) return M2_ERR_UNSUPPORTED;
+    // groups in a grid dimension, channel and group offsets of a row in 32 bits
+    if (s->ngroups > 65535 || s->channels > (1 << 24) || static_cast<int64_t>(s->ngroups) * s->d_state > (1 << 24)) return M2_ERR_UNSUPPORTED;
     return M2_OK;
 }
 

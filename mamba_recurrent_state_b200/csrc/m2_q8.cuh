@@ -71,6 +71,8 @@ struct Q8UpdateArgs {
     float norm_eps;
     int tile_rows;       // state rows per CTA (plan_q8_update)
     int group_ctas;      // CTAs per SSM group: the thread-block cluster
+    int group_rows, hpg; // rows and heads of a group
+    uint32_t inv_P;      // 2^22 / P, rounded up
 };
 // Shape check of the decode step (host arithmetic): M2_OK or M2_ERR_UNSUPPORTED.
 m2_status q8_shape_supported(int H, int P, int N, int G);

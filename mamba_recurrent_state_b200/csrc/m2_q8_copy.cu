@@ -17,7 +17,10 @@
 namespace m2 {
 namespace {
 
-constexpr int kThreads = 256;
+// 128 Nemotron-H sequences (422 MB either way, 65.3 us at the copy bandwidth):
+// store 68.7 us, load 69.2 us with 128 threads and four passes; 256 threads and
+// four 70.7 / 77.1, one 77.0 / 69.8, eight 74.8 / 79.3; 64 and four 70.1 / 69.7 us.
+constexpr int kThreads = 128;
 constexpr int kUnroll = 4;
 
 template <int EPV>

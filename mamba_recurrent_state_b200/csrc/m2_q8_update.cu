@@ -8,7 +8,7 @@
 //
 // Work decomposition:
 //  * A sequence's state is H*P rows of N codes. The rows of an SSM group are
-//    cut into tiles of tile_rows rows (the last may be short), a CTA of 256
+//    cut into tiles of tile_rows rows (the last may be short), a CTA of 128
 //    threads each, the group's CTAs one thread-block cluster.
 //  * One thread puts the slot's conv rows, the tile's scales and the codes in
 //    flight as bulk copies before anything else is computed.
@@ -16,13 +16,20 @@
 //    thread works on two rows at once: their S' stay in registers while the
 //    sums y and the maxima a go over the LPR lanes, both with the first level
 //    exchanging halves, so that one lane in two ends with one row's result and
-//    divides for one row only; the inverses come back with one shuffle a row.
+//    forms one row's scale and inverse only (a product with 1/127 and the
+//    special-function unit's reciprocal, within 2^-22 of the quotients); the
+//    inverses come back with one shuffle a row.
 //  * Codes become floats by a byte permute into 2^23 and one exact subtraction
 //    and are rounded by one FMA with 1.5 * 2^23 (m2_q8.cuh): no conversion
 //    instructions, which issue at a quarter of the FMA rate.
 //  * Conv, cluster and waits as in m2_state_update.cu: every CTA computes the
 //    conv of its x channels and of the group's B and C; cluster rank 0 alone
 //    rolls the group's B/C conv rows, after all have read them.
+//
+// Bound by instruction issue beside HBM: a code takes 0.34 warp instructions, all
+// included (unpack, update, y, maximum, round, pack, exchanges, conv), which for
+// 64 Nemotron-H rows is 20 us of the SMs' issue slots beside 23 us of HBM time,
+// and a CTA's wait for its rows overlaps only with other CTAs' arithmetic.
 #include <cuda_runtime.h>
 
 #include <algorithm>
@@ -32,23 +39,20 @@
 namespace m2 {
 namespace {
 
-#ifndef Q8_THREADS
-#define Q8_THREADS 128
-#endif
-#ifndef Q8_MINB
-#define Q8_MINB 4
-#endif
-#ifndef Q8_CP
-#define Q8_CP 4
-#endif
-#ifndef Q8_TILE
-#define Q8_TILE 256
-#endif
-constexpr int kThreads = Q8_THREADS;
+// Threads of a CTA, rows of its tile, the resident CTAs per SM that the
+// registers are sized for (five do reside: 90 registers, 43 KB), passes over the
+// tile that one copy brings. 64 Nemotron-H rows (23.2 us at the copy bandwidth):
+// 128, 256, 4, 8 passes 35.8 us; sized for three CTAs 39.1 (126 registers, four
+// reside), for five 42.1 (the compiler trades registers for instructions); 192
+// rows 43.4; 256 threads 57.5, with 512 rows 52.3 us; two rings of 256 rows, the
+// next row's copies under this one's arithmetic, 54.3 us.
+constexpr int kThreads = 128;
+constexpr int kTileRows = 256;
+constexpr int kMinBlocks = 4;
 constexpr int kWarps = kThreads / 32;
 constexpr int kRowsPerThread = 2;
-constexpr int kMaxPasses = 16;      // passes of a CTA over its tile
-constexpr int kCopyPasses = Q8_CP;  // passes that one copy and its barrier bring
+constexpr int kMaxPasses = 16;
+constexpr int kCopyPasses = 8;
 constexpr int kMaxCopies = kMaxPasses / kCopyPasses;
 constexpr int kMaxHeads = 66;       // heads that a tile of 512 rows can touch (P >= 8)
 constexpr int kMaxCluster = 16;
@@ -111,14 +115,21 @@ __device__ __forceinline__ float reduce_two(float v0, float v1, bool upper, Op o
     return v;
 }
 
+// Where B and C of state n are kept: the 16 of a lane as four 16-byte vectors,
+// vector q of all lanes side by side (no bank conflicts).
+template <int LPR>
+__device__ __forceinline__ int bc_place(int n) {
+    return ((n / 4 % 4) * LPR + n / 16) * 4 + n % 4;
+}
+
 template <typename AT, int N, bool NORM>
-__global__ void __launch_bounds__(kThreads, Q8_MINB) q8_update_kernel(const Q8UpdateArgs a) {
+__global__ void __launch_bounds__(kThreads, kMinBlocks) q8_update_kernel(const Q8UpdateArgs a) {
     constexpr int LPR = N / 16;
     constexpr int RPP = kThreads / LPR;              // rows a CTA covers once
     constexpr int PASS = RPP * kRowsPerThread;       // rows of one pass
     constexpr int CW = 4 / sizeof(AT);               // channels per 32-bit word
     constexpr int AS = sizeof(AT);
-    constexpr int kPre = (Q8_TILE + 2 * N) / CW >= 3 * kThreads ? 3 : ((Q8_TILE + 2 * N) / CW >= 2 * kThreads ? 2 : 1);
+    constexpr int kPre = (kTileRows + 2 * N) / CW >= 3 * kThreads ? 3 : ((kTileRows + 2 * N) / CW >= 2 * kThreads ? 2 : 1);
 
     extern __shared__ __align__(128) uint8_t s_dyn[];
     __shared__ __align__(8) uint64_t s_bar[kMaxCopies + 1];
@@ -129,14 +140,17 @@ __global__ void __launch_bounds__(kThreads, Q8_MINB) q8_update_kernel(const Q8Up
     const int tid = threadIdx.x;
     const int K = a.K, P = a.P;
     const int64_t HP = static_cast<int64_t>(a.H) * P;
-    const int group_rows = a.H / a.G * P;
-    const int g = blockIdx.x / a.group_ctas;
-    const int off = (blockIdx.x % a.group_ctas) * a.tile_rows;  // first row within the group
-    const int nrows = min(a.tile_rows, group_rows - off);       // a multiple of 8, at least 8
+    const int group_rows = a.group_rows;
+    const int g = blockIdx.y;
+    const int off = blockIdx.x * a.tile_rows;              // first row within the group
+    const int nrows = min(a.tile_rows, group_rows - off);  // a multiple of 8, at least 8
     const int64_t r0 = static_cast<int64_t>(g) * group_rows + off;
-    const int h_first = static_cast<int>(r0 / P);
-    const int rr0 = static_cast<int>(r0 - static_cast<int64_t>(h_first) * P);
-    const int n_heads = (rr0 + nrows - 1) / P + 1;
+    // rows to heads: v / P for v < 2^13 by the host's reciprocal 2^22 / P
+    auto head_of = [&](uint32_t v) -> int { return static_cast<int>((v * a.inv_P) >> 22); };
+    const int h_in_group = head_of(off);
+    const int h_first = g * a.hpg + h_in_group;
+    const int rr0 = off - h_in_group * P;
+    const int n_heads = head_of(rr0 + nrows - 1) + 1;
     const int64_t cd = a.conv_dim;
     const int64_t cB = HP + static_cast<int64_t>(g) * N;
     const int64_t cC = cB + static_cast<int64_t>(a.G) * N;
@@ -151,10 +165,22 @@ __global__ void __launch_bounds__(kThreads, Q8_MINB) q8_update_kernel(const Q8Up
     float* s_C = reinterpret_cast<float*>(s_dyn + L.C);
     uint32_t* s_rawbc = reinterpret_cast<uint32_t*>(s_dyn + L.raw_bc);
 
+    constexpr int COPY = PASS * kCopyPasses;  // rows of one copy
+    const int passes = (nrows + PASS - 1) / PASS;
+    const int copies = (nrows + COPY - 1) / COPY;
+    uint64_t* bar_conv = &s_bar[kMaxCopies];
+    if (tid == 0) {
+        s_fail = 0;
+        for (int c = 0; c < copies; ++c) mbar_init(&s_bar[c], 1);
+        mbar_init(bar_conv, 1);
+        fence_mbar_init();
+    }
+    __syncthreads();
+
     // A programmatic dependent of the previous kernel: nothing is read before.
     asm volatile("griddepcontrol.wait;\n" ::: "memory");
 
-    const int64_t b = blockIdx.y;
+    const int64_t b = blockIdx.z;
     const AT* xrow = static_cast<const AT*>(a.xBC) + b * a.xBC_stride;
     const AT* zrow = a.z ? static_cast<const AT*>(a.z) + b * a.z_stride : nullptr;
     AT* yrow = static_cast<AT*>(a.y) + b * a.y_stride;
@@ -204,15 +230,7 @@ __global__ void __launch_bounds__(kThreads, Q8_MINB) q8_update_kernel(const Q8Up
     int8_t* tile = a.ssm + row_base * N;
     float* scales = a.scale + row_base;
     AT* conv0 = static_cast<AT*>(a.conv) + static_cast<int64_t>(slot) * (K - 1) * cd;
-    uint64_t* bar_conv = &s_bar[kMaxCopies];
-    constexpr int COPY = PASS * kCopyPasses;  // rows of one copy
-    const int passes = (nrows + PASS - 1) / PASS;
-    const int copies = (nrows + COPY - 1) / COPY;
     if (tid == 0) {
-        s_fail = 0;
-        for (int c = 0; c < copies; ++c) mbar_init(&s_bar[c], 1);
-        mbar_init(bar_conv, 1);
-        fence_mbar_init();
         mbar_arrive_expect_tx(bar_conv, static_cast<uint32_t>((K - 1) * (nrows + 2 * N) * AS + nrows * 4));
         bulk_g2s(s_dyn + L.scale, scales, nrows * 4, bar_conv);
         for (int k = 0; k < K - 1; ++k) {
@@ -240,7 +258,7 @@ __global__ void __launch_bounds__(kThreads, Q8_MINB) q8_update_kernel(const Q8Up
         auto conv_word = [&](int q, uint32_t raw, uint32_t bias_w, uint4 wv) {
             const bool is_x = q < nx;
             const int j = is_x ? q * CW : (q - nx) * CW;  // channel within the segment(s)
-            const int seg = j / N;                        // (B, C) 0 or 1
+            const int seg = j >= N ? 1 : 0;               // (B, C) 0 or 1
             const int64_t c0 = word_channel(q);
             const AT* rows = is_x ? s_cx + j : s_cbc + seg * (K - 1) * N + (j - seg * N);
             const int pitch = is_x ? a.tile_rows : N;
@@ -275,7 +293,7 @@ __global__ void __launch_bounds__(kThreads, Q8_MINB) q8_update_kernel(const Q8Up
                 for (int k = 0; k < K - 1; ++k)  // roll this CTA's own conv rows
                     *reinterpret_cast<uint32_t*>(conv0 + k * cd + c0) =
                         k < K - 2 ? *reinterpret_cast<const uint32_t*>(rows + (k + 1) * pitch) : raw;
-                const int hl = (rr0 + j) / P;  // CW channels lie in one head
+                const int hl = head_of(rr0 + j);  // CW channels lie in one head
                 const float dtv = s_dt[hl], dAv = s_dA[hl], Dv = s_D[hl];
 #pragma unroll
                 for (int e = 0; e < CW; ++e) {
@@ -283,7 +301,7 @@ __global__ void __launch_bounds__(kThreads, Q8_MINB) q8_update_kernel(const Q8Up
                     s_y[j + e] = Dv * out[e];
                 }
             } else {
-                float* dst = (seg ? s_C : s_B) + (j - seg * N);
+                float* dst = (seg ? s_C : s_B) + bc_place<LPR>(j - seg * N);
 #pragma unroll
                 for (int e = 0; e < CW; ++e) dst[e] = out[e];
                 s_rawbc[j / CW] = raw;
@@ -316,9 +334,13 @@ __global__ void __launch_bounds__(kThreads, Q8_MINB) q8_update_kernel(const Q8Up
     const bool upper = (lane & (LPR / 2)) != 0;
     float2 B2[8], C2[8];
 #pragma unroll
-    for (int e = 0; e < 8; ++e) {
-        B2[e] = *reinterpret_cast<const float2*>(s_B + l * 16 + 2 * e);
-        C2[e] = *reinterpret_cast<const float2*>(s_C + l * 16 + 2 * e);
+    for (int q = 0; q < 4; ++q) {
+        const float4 vb = *reinterpret_cast<const float4*>(s_B + (q * LPR + l) * 4);
+        const float4 vc = *reinterpret_cast<const float4*>(s_C + (q * LPR + l) * 4);
+        B2[2 * q] = make_float2(vb.x, vb.y);
+        B2[2 * q + 1] = make_float2(vb.z, vb.w);
+        C2[2 * q] = make_float2(vc.x, vc.y);
+        C2[2 * q + 1] = make_float2(vc.z, vc.w);
     }
     // row (c * 2 + i) * RPP + tid / LPR of the tile is codes ((c * 2 + i) * kThreads + tid) * 16 .. + 15
     const float2* rps = s_rp + tid / LPR;
@@ -340,7 +362,7 @@ __global__ void __launch_bounds__(kThreads, Q8_MINB) q8_update_kernel(const Q8Up
             const uint4 w = *reinterpret_cast<const uint4*>(codes + (c * kRowsPerThread + i) * (kThreads * 16));
             const uint32_t words[4] = {w.x, w.y, w.z, w.w};
             const float2 dtx = make_float2(rp.x, rp.x), k2 = make_float2(rp.y, rp.y);
-            float2 acc = make_float2(0.f, 0.f);
+            float2 acc;
             float m = 0.f;
 #pragma unroll
             for (int q = 0; q < 4; ++q) {
@@ -348,7 +370,7 @@ __global__ void __launch_bounds__(kThreads, Q8_MINB) q8_update_kernel(const Q8Up
                 q8_unpack(words[q], lo, hi);
                 lo = __ffma2_rn(lo, k2, __fmul2_rn(dtx, B2[2 * q]));
                 hi = __ffma2_rn(hi, k2, __fmul2_rn(dtx, B2[2 * q + 1]));
-                acc = __ffma2_rn(lo, C2[2 * q], acc);
+                acc = q == 0 ? __fmul2_rn(lo, C2[0]) : __ffma2_rn(lo, C2[2 * q], acc);
                 acc = __ffma2_rn(hi, C2[2 * q + 1], acc);
                 m = max_abs(m, lo.x, lo.y);
                 m = max_abs(m, hi.x, hi.y);
@@ -461,7 +483,7 @@ cudaError_t launch_one(const Q8UpdateArgs& a, cudaStream_t stream) {
     });
     if (e != cudaSuccess) return e;
     cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3(a.G * a.group_ctas, a.batch, 1);
+    cfg.gridDim = dim3(a.group_ctas, a.G, a.batch);
     cfg.blockDim = dim3(kThreads, 1, 1);
     cfg.dynamicSmemBytes = Layout(a.tile_rows, N, a.K, sizeof(AT)).bytes;
     cfg.stream = stream;
@@ -508,9 +530,21 @@ m2_status q8_shape_supported(int H, int P, int N, int G) {
 
 cudaError_t launch_q8_update(Q8UpdateArgs a, cudaStream_t stream) {
     const int group_rows = a.H / a.G * a.P;
-    int tile = std::min(Q8_TILE, max_tile(a.N));
+    int tile = std::min(kTileRows, max_tile(a.N));
     if (group_rows < tile) tile = (group_rows + pass_rows(a.N) - 1) / pass_rows(a.N) * pass_rows(a.N);
     while ((group_rows + tile - 1) / tile > kMaxCluster) tile *= 2;
+    int dev = 0, sms = 148;
+    if (cudaGetDevice(&dev) != cudaSuccess || cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess)
+        sms = 148;
+    // few rows: halve the tiles as long as that brings idle SMs in and the
+    // cluster stays portable (one Nemotron-H row: 6.2 us with 256 rows a tile, 4.9
+    // with 128; five 7.2 and 6.2)
+    while (tile % (2 * pass_rows(a.N)) == 0 && 2 * ((group_rows + tile - 1) / tile) <= 8 &&
+           static_cast<int64_t>(a.G) * ((group_rows + tile - 1) / tile) * a.batch < 2 * sms)
+        tile /= 2;
+    a.group_rows = group_rows;
+    a.hpg = a.H / a.G;
+    a.inv_P = ((1u << 22) + a.P - 1) / a.P;
     a.tile_rows = tile;
     a.group_ctas = (group_rows + tile - 1) / tile;
     return a.act_bf16 ? by_n<bf16_t>(a, stream) : by_n<float>(a, stream);

@@ -56,8 +56,10 @@ template <typename AT>
 struct Decay {
     static constexpr bool kExact = sizeof(AT) == 4;
     // what a state keeps of its A, and the decay over dt by it
+    // (kept finite, so that a dt of zero leaves the state as it is)
     __device__ static __forceinline__ float factor(float A_log) {
-        return kExact ? -expf(A_log) : -kLog2E * ex2_approx(A_log * kLog2E);
+        const float f = kExact ? -expf(A_log) : -kLog2E * ex2_approx(A_log * kLog2E);
+        return f < -3e38f ? -3e38f : f;
     }
     __device__ static __forceinline__ float over(float x) { return kExact ? expf(x) : ex2_approx(x); }  // x = dt * factor
     __device__ static __forceinline__ float2 softplus(float2 v);

@@ -73,7 +73,8 @@ def test_wrap_and_sizes_on_the_host():
     for shape, want in ((m2.Shape(8, 64, 256, 1, 4, F32, F32), m2.M2_OK),  # an 8-bit state has one width
                         (m2.Shape(8, 64, 96, 1, 4), m2.M2_ERR_UNSUPPORTED), (m2.Shape(8, 12, 64, 1, 4), m2.M2_ERR_UNSUPPORTED),
                         (m2.Shape(256, 64, 128, 1, 4), m2.M2_ERR_UNSUPPORTED), (m2.Shape(8, 64, 128, 3, 4), m2.M2_ERR_INVALID_ARG),
-                        (m2.Shape(8, 64, 128, 1, 9), m2.M2_ERR_UNSUPPORTED)):
+                        (m2.Shape(8, 64, 128, 1, 9), m2.M2_ERR_UNSUPPORTED),
+                        (m2.Shape(65536, 8, 64, 65536, 4), m2.M2_ERR_UNSUPPORTED)):
         s = shape.c()
         assert L.m2_q8_shape_check(ctypes.byref(s)) == want
 
@@ -415,6 +416,62 @@ def test_decode_in_a_graph_and_on_another_stream():
         assert torch.equal(y, want[i])
     assert torch.equal(cache.ssm, eager.ssm) and torch.equal(cache.scale, eager.scale)
     assert torch.equal(full.ssm[0], (eager.ssm[0].float() * eager.scale[0][..., None]).bfloat16())
+
+
+@pytest.mark.gpu
+def test_slots_past_32_bits():
+    """The last slot of a cache whose codes pass 2^31 bytes: the same bits as the first slot of a small one."""
+    shape = m2.Shape(128, 64, 128, 8, 4, BF16, BF16)
+    _, small = caches(shape, 0, 1)
+    big = m2.Q8Cache(shape, 2100)
+    last, zero = torch.tensor([2099], dtype=torch.int32, device="cuda"), torch.zeros(1, dtype=torch.int32, device="cuda")
+    for a, b in ((big.ssm, small.ssm), (big.scale, small.scale), (big.conv, small.conv)):
+        a[2099] = b[0]
+    layer = Layer(shape, 1)
+    assert torch.equal(layer.run(big, last), layer.run(small, zero))
+    full = m2.Cache(shape, 2)
+    m2.q8_load(big, full, last, zero)
+    m2.q8_store(full, big, zero, torch.tensor([2098], dtype=torch.int32, device="cuda"))
+    want = m2.Cache(shape, 1)
+    m2.q8_load(small, want, zero, zero)
+    assert torch.equal(full.ssm[0], want.ssm[0]) and torch.equal(big.ssm[2098], reference_codes(want.ssm[0].float())[0])
+    assert torch.equal(big.conv[2098], small.conv[0]) and not big.ssm[:2098].any()
+
+
+@pytest.mark.gpu
+def test_validate_mode_refuses_duplicates(monkeypatch):
+    shape = m2.Shape(8, 64, 128, 1, 4, BF16, BF16)
+    full, cache = caches(shape, 3, 3)
+    layer = Layer(shape, 2)
+    at = lambda *v: torch.tensor(v, dtype=torch.int32, device="cuda")  # noqa: E731
+    monkeypatch.setenv("M2_VALIDATE", "1")
+    with pytest.raises(m2.M2Error):
+        layer.run(cache, at(1, 1))
+    with pytest.raises(m2.M2Error):
+        m2.q8_store(full, cache, at(0, 1), at(2, 2))
+    m2.q8_load(cache, full, at(2, 2), at(0, 1))  # a snapshot may be read twice
+    layer.run(cache, at(1, -1))
+
+
+@pytest.mark.gpu
+def test_two_streams_at_once():
+    """Two batches on two caches on two streams, and again in turn: the same bits."""
+    shape = m2.Shape(16, 64, 128, 2, 4, BF16, BF16)
+    slots = torch.arange(40, dtype=torch.int32, device="cuda")
+    layers = [Layer(shape, 40, seed=s) for s in (1, 2)]
+    pairs = [[caches(shape, 0, 40, seed=s)[1] for s in (1, 2)] for _ in range(2)]
+    want = [[layers[i].run(pairs[0][i], slots) for _ in range(3)] for i in range(2)]
+    torch.cuda.synchronize()
+    streams = [torch.cuda.Stream() for _ in range(2)]
+    got = [[], []]
+    for _ in range(3):
+        for i in range(2):
+            with torch.cuda.stream(streams[i]):
+                got[i].append(layers[i].run(pairs[1][i], slots))
+    torch.cuda.synchronize()
+    for i in range(2):
+        assert all(torch.equal(u, v) for u, v in zip(got[i], want[i]))
+        assert torch.equal(pairs[0][i].ssm, pairs[1][i].ssm) and torch.equal(pairs[0][i].scale, pairs[1][i].scale)
 
 
 # ---- the path as it is used ------------------------------------------------------

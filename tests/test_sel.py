@@ -115,7 +115,7 @@ def test_shapes_and_sizes_on_the_host():
                         (m2.SelShape(12, 128, 3, 8, F32, F32), m2.M2_OK), (m2.SelShape(12, 16), m2.M2_ERR_UNSUPPORTED),
                         (m2.SelShape(64, 24), m2.M2_ERR_UNSUPPORTED), (m2.SelShape(64, 16, 3), m2.M2_ERR_INVALID_ARG),
                         (m2.SelShape(64, 16, 1, 1), m2.M2_ERR_UNSUPPORTED), (m2.SelShape(0, 16), m2.M2_ERR_INVALID_ARG),
-                        (m2.SelShape(64, 16, 1, 4, m2.M2_F16), m2.M2_ERR_INVALID_ARG)):
+                        (m2.SelShape(64, 16, 1, 4, m2.M2_F16), m2.M2_ERR_INVALID_ARG), (m2.SelShape(2**20, 8, 2**17), m2.M2_ERR_UNSUPPORTED)):
         assert m2.sel_shape_check(shape) == want, shape
     s = m2.SelShape(1000, 16, 1, 4, F32, BF16).c()
     a, b = ctypes.c_int64(), ctypes.c_int64()
@@ -379,6 +379,70 @@ def test_conv_of_prompts_and_tokens(act):
         assert ((got.double() - want).abs() <= bound).all()
         assert torch.equal(cache.conv[int(slots[i])], raw[-3:])
     assert torch.equal(cache.conv[2], before[2])
+
+
+@pytest.mark.gpu
+def test_slots_past_32_bits():
+    shape = m2.SelShape(8192, 16, 1, 4, F32, BF16)
+    far = 2**31 // (8192 * 16) + 3  # its first element lies past 2^31
+    big, small = m2.SelCache(shape, far + 1), cache_of(shape, 1)
+    big.ssm[far], big.conv[far] = small.ssm[0], small.conv[0]
+    layer = Layer(shape, 30)
+    one = torch.ones(1, dtype=torch.uint8, device="cuda")
+    for cache, slot in ((big, far), (small, 0)):
+        at = ints(slot)
+        x = m2.sel_conv1d_update_varlen(cache, layer.taps, layer.x, offsets([30]), at, 30)
+        y = m2.sel_scan(cache, layer.params, x, layer.dt, layer.B, layer.C, offsets([30]), at, z=layer.z, has_initial_state=one)
+        y2 = m2.sel_state_update(cache, layer.params, x[:1], layer.dt[:1], layer.B[:1], layer.C[:1], at)
+        if cache is big:
+            want = (y, y2)
+    assert torch.equal(y, want[0]) and torch.equal(y2, want[1])
+    assert torch.equal(big.ssm[far], small.ssm[0]) and torch.equal(big.conv[far], small.conv[0]) and not big.ssm[:far:4096].any()
+
+
+@pytest.mark.gpu
+def test_validate_mode_refuses_duplicates(monkeypatch):
+    shape = m2.SelShape(64, 16, 1, 4, F32, BF16)
+    layer, cache = Layer(shape, 4), cache_of(shape, 3)
+    monkeypatch.setenv("M2_VALIDATE", "1")
+    rest = (layer.x, layer.dt, layer.B, layer.C)
+    with pytest.raises(m2.M2Error):
+        m2.sel_scan(cache, layer.params, *rest, offsets([2, 2]), ints(1, 1))
+    with pytest.raises(m2.M2Error):
+        m2.sel_state_update(cache, layer.params, *(t[:2] for t in rest), ints(1, 1))
+    with pytest.raises(m2.M2Error):
+        m2.sel_conv1d_update(cache, layer.taps, layer.x[:2], ints(2, 2))
+    m2.sel_scan(cache, layer.params, *rest, offsets([2, 2]), ints(1, -1))
+
+
+@pytest.mark.gpu
+def test_scans_on_two_streams_and_in_a_graph():
+    """Segmented scans (clusters) beside each other, and captured: the same bits as in turn."""
+    shape = m2.SelShape(128, 16, 1, 4, F32, BF16)
+    layers = [Layer(shape, 900, seed=s) for s in (1, 2)]
+    cu, slots = offsets([900]), ints(0)
+    run = lambda i, c, **kw: m2.sel_scan(c, layers[i].params, layers[i].x, layers[i].dt, layers[i].B, layers[i].C, cu, slots,  # noqa: E731
+                                         z=layers[i].z, has_initial_state=one, **kw)
+    one = torch.ones(1, dtype=torch.uint8, device="cuda")
+    first, second = [cache_of(shape, 1, s) for s in (1, 2)], [cache_of(shape, 1, s) for s in (1, 2)]
+    want = [[run(i, first[i]) for _ in range(3)] for i in range(2)]
+    torch.cuda.synchronize()
+    streams = [torch.cuda.Stream() for _ in range(2)]
+    got = [[], []]
+    for _ in range(2):
+        for i in range(2):
+            with torch.cuda.stream(streams[i]):
+                got[i].append(run(i, second[i]))
+    torch.cuda.synchronize()
+    y = torch.empty_like(want[0][0])
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        run(0, second[0], y=y)
+    graph.replay()
+    assert torch.equal(y, want[0][2])
+    run(1, second[1])
+    for i in range(2):
+        assert all(torch.equal(u, v) for u, v in zip(got[i], want[i])) and torch.equal(first[i].ssm, second[i].ssm)
 
 
 # ---- the path as it is used ------------------------------------------------------
