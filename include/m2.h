@@ -474,8 +474,9 @@ m2_status m2_host_stage_join(m2_host_stage* stage, m2_stream stream);
  *   a = max |v| over the row, both quotients rounded to fp32, then
  *   scale = a / 127,  code = round half to even (v * (127 / a)),
  * and a value reads back as code * scale, at most scale / 2 (and fp32
- * rounding) from v. A row with a < 2^-100 is stored as zeros. A row that holds
- * an infinity or a NaN reads back as NaN in every value: its scale is NaN.
+ * rounding) from v. (The decode step forms the quotients within 2^-22.) A row
+ * with a < 2^-100 is stored as zeros, scale and codes. A row that holds an
+ * infinity or a NaN reads back as NaN in every value: its scale is NaN.
  * Every store rounds: a state that stays parked is rounded once, one that
  * decodes on the 8-bit cache once a token.
  */
@@ -518,7 +519,8 @@ m2_status m2_q8_zero_slots(const m2_q8_cache* cache, int32_t n, const int32_t* s
  * same H, P, N, G, K and act_dtype (M2_ERR_INVALID_ARG otherwise). A pair with
  * a negative index is skipped; an index past its cache's slots records
  * M2_ERR_BAD_SLOT in that cache's error word and skips the pair. src_idx may
- * repeat a slot; the non-negative dst_idx must be distinct. One launch.
+ * repeat a slot; the non-negative dst_idx must be distinct (M2_VALIDATE=1
+ * checks). Both caches are on the current device. One launch.
  */
 m2_status m2_q8_store(const m2_cache* src, const m2_q8_cache* dst, int32_t n, const int32_t* src_idx,
                       const int32_t* dst_idx, m2_stream stream);
@@ -632,9 +634,15 @@ m2_status m2_sel_state_update(const m2_sel_cache* cache, const m2_sel_params* pa
  * (from zero when has_initial_state is NULL or has_initial_state[b] == 0) and
  * leaves its final state there, rounded once. An empty sequence leaves its
  * slot untouched; rows of y past the last sequence are not written.
- * max_seqlen is a host bound on the lengths that only chooses how channels are
- * spread over the GPU. The sums run in the order of the tokens in fp32. At most
- * 65535 sequences. One launch, no scratch memory.
+ * max_seqlen is a host bound on the lengths: it never decides what is computed,
+ * only how channels are spread over the GPU. The state runs in fp32; a long
+ * sequence of few channels is computed in segments, whose states are joined by
+ * the decay of their summed dt, and a sum over N goes over the lanes of a
+ * channel, so results of calls of other sizes can differ by fp32 rounding. With
+ * fp32 activations every softplus and decay is the library's expf and log1pf;
+ * with bf16 ones they come within 5e-7 from the special-function unit, and
+ * silu(z) within 2^-10 of itself (for z < -6 within 2^-15): half a bf16 step is
+ * 2^-9. At most 65535 sequences. One launch, no scratch memory.
  */
 m2_status m2_sel_scan(const m2_sel_cache* cache, const m2_sel_params* params, int32_t nseq,
                       const int32_t* cu_seqlens, int64_t total_tokens, int32_t max_seqlen, const void* x,

@@ -712,7 +712,7 @@ def _q8_copy(name: str, src, dst, src_idx: torch.Tensor, dst_idx: torch.Tensor, 
     _index(src_idx, "src_idx", n, q8.device)
     _index(dst_idx, "dst_idx", n, q8.device)
     full = dst if q8 is src else src
-    if full.ssm is not None and full.ssm.device != q8.device:
+    if (full.c.device != q8.device.index) if full.native else (full.ssm.device != q8.device):
         raise ValueError("the two caches are on different devices")
     _current(q8.device)
     _check(getattr(lib(), name)(ctypes.byref(src.c), ctypes.byref(dst.c), n, src_idx.data_ptr(), dst_idx.data_ptr(),

@@ -78,30 +78,36 @@ __device__ __forceinline__ void st_cluster_f32(float* local, uint32_t rank, floa
     asm volatile("st.shared::cluster.f32 [%0], %1;\n" ::"r"(remote), "f"(v) : "memory");
 }
 
-// One 32-bit word of activations: two bf16 channels or one fp32.
+// Four channels of activations as one vector.
 template <typename AT>
-__device__ __forceinline__ void unpack_word(uint32_t u, float* out) {
-    if constexpr (sizeof(AT) == 2) {
-        out[0] = __uint_as_float(u << 16);
-        out[1] = __uint_as_float(u & 0xFFFF0000u);
-    } else {
-        out[0] = __uint_as_float(u);
+struct Quad;
+template <>
+struct Quad<bf16_t> {
+    using T = uint2;
+    __device__ static __forceinline__ float4 unpack(uint2 u) {
+        return make_float4(__uint_as_float(u.x << 16), __uint_as_float(u.x & 0xFFFF0000u), __uint_as_float(u.y << 16),
+                           __uint_as_float(u.y & 0xFFFF0000u));
     }
-}
+    __device__ static __forceinline__ uint2 pack(float4 v) { return make_uint2(pack_bf16x2(v.x, v.y), pack_bf16x2(v.z, v.w)); }
+};
+template <>
+struct Quad<float> {
+    using T = float4;
+    __device__ static __forceinline__ float4 unpack(float4 v) { return v; }
+    __device__ static __forceinline__ float4 pack(float4 v) { return v; }
+};
 
 // Byte offsets of the dynamic shared memory of a CTA.
 struct Layout {
-    int scale, conv_x, conv_bc, rp, y, B, C, raw_bc, bytes;
+    int scale, roll, rp, y, B, C, bytes;
     __host__ __device__ Layout(int tile, int N, int K, int as) {
-        scale = tile * N;                       // the old scales, later the new ones
-        conv_x = scale + tile * 4;              // [K-1][tile]
-        conv_bc = conv_x + (K - 1) * tile * as; // [2][K-1][N]
-        rp = conv_bc + 2 * (K - 1) * N * as;    // per row {dt*x, scale*dA}
-        y = rp + tile * 8;                      // D*x, later y
+        scale = tile * N;                // the new scales
+        rp = scale + tile * 4;           // per row {dt*x, scale*dA}
+        y = rp + tile * 8;               // D*x, later y
         B = y + tile * 4;
         C = B + N * 4;
-        raw_bc = C + N * 4;                     // this step's raw B and C inputs
-        bytes = raw_bc + 2 * N * as;
+        roll = C + N * 4;                // [K-1][2][N]: the group's rolled B and C conv rows (cluster rank 0)
+        bytes = roll + 2 * (K - 1) * N * as;
     }
 };
 
@@ -127,14 +133,13 @@ __global__ void __launch_bounds__(kThreads, kMinBlocks) q8_update_kernel(const Q
     constexpr int LPR = N / 16;
     constexpr int RPP = kThreads / LPR;              // rows a CTA covers once
     constexpr int PASS = RPP * kRowsPerThread;       // rows of one pass
-    constexpr int CW = 4 / sizeof(AT);               // channels per 32-bit word
     constexpr int AS = sizeof(AT);
-    constexpr int kPre = (kTileRows + 2 * N) / CW >= 3 * kThreads ? 3 : ((kTileRows + 2 * N) / CW >= 2 * kThreads ? 2 : 1);
+    using Q = Quad<AT>;
+    using V4 = typename Q::T;
 
     extern __shared__ __align__(128) uint8_t s_dyn[];
-    __shared__ __align__(8) uint64_t s_bar[kMaxCopies + 1];
+    __shared__ __align__(8) uint64_t s_bar[kMaxCopies];
     __shared__ float s_dt[kMaxHeads], s_dA[kMaxHeads], s_D[kMaxHeads];
-    __shared__ int s_fail;
     __shared__ float s_red[kWarps], s_parts[kMaxCluster], s_rstd;
 
     const int tid = threadIdx.x;
@@ -157,22 +162,17 @@ __global__ void __launch_bounds__(kThreads, kMinBlocks) q8_update_kernel(const Q
     const Layout L(a.tile_rows, N, K, AS);
     const uint8_t* s_codes = s_dyn;
     float* s_scale = reinterpret_cast<float*>(s_dyn + L.scale);
-    const AT* s_cx = reinterpret_cast<const AT*>(s_dyn + L.conv_x);
-    const AT* s_cbc = reinterpret_cast<const AT*>(s_dyn + L.conv_bc);
     float2* s_rp = reinterpret_cast<float2*>(s_dyn + L.rp);
     float* s_y = reinterpret_cast<float*>(s_dyn + L.y);
     float* s_B = reinterpret_cast<float*>(s_dyn + L.B);
     float* s_C = reinterpret_cast<float*>(s_dyn + L.C);
-    uint32_t* s_rawbc = reinterpret_cast<uint32_t*>(s_dyn + L.raw_bc);
+    V4* s_roll = reinterpret_cast<V4*>(s_dyn + L.roll);
 
     constexpr int COPY = PASS * kCopyPasses;  // rows of one copy
     const int passes = (nrows + PASS - 1) / PASS;
     const int copies = (nrows + COPY - 1) / COPY;
-    uint64_t* bar_conv = &s_bar[kMaxCopies];
     if (tid == 0) {
-        s_fail = 0;
         for (int c = 0; c < copies; ++c) mbar_init(&s_bar[c], 1);
-        mbar_init(bar_conv, 1);
         fence_mbar_init();
     }
     __syncthreads();
@@ -185,29 +185,35 @@ __global__ void __launch_bounds__(kThreads, kMinBlocks) q8_update_kernel(const Q
     const AT* zrow = a.z ? static_cast<const AT*>(a.z) + b * a.z_stride : nullptr;
     AT* yrow = static_cast<AT*>(a.y) + b * a.y_stride;
     // ---- what does not depend on the slot is loaded before the slot is read:
-    // its latency hides behind the slot's and the copies'
-    const int n_words = (nrows + 2 * N) / CW;  // conv words: x of the tile, then B and C
-    const int nx = nrows / CW;
+    // its latency hides behind the slot's and the codes'. A thread's first four
+    // conv channels (of the tile's x, then the group's B and C):
+    const int nx = nrows / 4, n_quads = nx + N / 2;
     const AT* w = static_cast<const AT*>(a.conv_w);
     const AT* bias = static_cast<const AT*>(a.conv_b);
-    auto word_channel = [&](int q) -> int64_t {
-        if (q < nx) return r0 + q * CW;
-        const int j = (q - nx) * CW;
-        return j < N ? cB + j : cC + (j - N);
+    auto quad_channel = [&](int q) -> int {
+        const int j = (q - nx) * 4;
+        return static_cast<int>(q < nx ? r0 + q * 4 : (j < N ? cB + j : cC + (j - N)));
     };
-    uint32_t raw_in[kPre], bias_in[kPre];
-    uint4 w_in[kPre];
+    auto quad_of = [](const AT* p) -> V4 { return *reinterpret_cast<const V4*>(p); };
+    struct Taps {
+        uint4 v[AS];  // 4 channels x 4 taps
+    };
+    auto taps_of = [&](int c0) {
+        Taps t;
 #pragma unroll
-    for (int i = 0; i < kPre; ++i) {
-        const int q = i * kThreads + tid;
-        raw_in[i] = bias_in[i] = 0;
-        w_in[i] = make_uint4(0, 0, 0, 0);
-        if (q < n_words) {
-            const int64_t c0 = word_channel(q);
-            raw_in[i] = *reinterpret_cast<const uint32_t*>(xrow + c0);
-            if (bias) bias_in[i] = __ldg(reinterpret_cast<const uint32_t*>(bias + c0));
-            if (K == 4) w_in[i] = __ldg(reinterpret_cast<const uint4*>(w + c0 * 4));
-        }
+        for (int i = 0; i < AS; ++i) t.v[i] = __ldg(reinterpret_cast<const uint4*>(w + static_cast<int64_t>(c0) * 4) + i);
+        return t;
+    };
+    const int c_first = quad_channel(tid);
+    const bool q_first = tid < n_quads;
+    V4 raw_in{}, bias_in{}, z_in{}, old_in[3]{};
+    Taps w_in{};
+    float4 scale_in = make_float4(0.f, 0.f, 0.f, 0.f);
+    if (q_first) {
+        raw_in = quad_of(xrow + c_first);
+        if (bias) bias_in = quad_of(bias + c_first);
+        if (K == 4) w_in = taps_of(c_first);
+        if (zrow && tid < nx) z_in = quad_of(zrow + c_first);
     }
     float hs_dt = 0.f, hs_bias = 0.f, hs_alog = 0.f, hs_D = 0.f;
     if (tid < n_heads) {
@@ -231,18 +237,19 @@ __global__ void __launch_bounds__(kThreads, kMinBlocks) q8_update_kernel(const Q
     float* scales = a.scale + row_base;
     AT* conv0 = static_cast<AT*>(a.conv) + static_cast<int64_t>(slot) * (K - 1) * cd;
     if (tid == 0) {
-        mbar_arrive_expect_tx(bar_conv, static_cast<uint32_t>((K - 1) * (nrows + 2 * N) * AS + nrows * 4));
-        bulk_g2s(s_dyn + L.scale, scales, nrows * 4, bar_conv);
-        for (int k = 0; k < K - 1; ++k) {
-            bulk_g2s(s_dyn + L.conv_x + k * a.tile_rows * AS, conv0 + k * cd + r0, nrows * AS, bar_conv);
-            bulk_g2s(s_dyn + L.conv_bc + k * N * AS, conv0 + k * cd + cB, N * AS, bar_conv);
-            bulk_g2s(s_dyn + L.conv_bc + (K - 1 + k) * N * AS, conv0 + k * cd + cC, N * AS, bar_conv);
-        }
         for (int c = 0; c < copies; ++c) {
             const int rows = min(COPY, nrows - c * COPY);
             mbar_arrive_expect_tx(&s_bar[c], rows * N);
             bulk_g2s(s_dyn + c * COPY * N, tile + static_cast<int64_t>(c) * COPY * N, rows * N, &s_bar[c]);
         }
+    }
+    auto old_quad = [&](int k, int c) -> V4 { return quad_of(conv0 + k * cd + c); };
+    if (q_first) {
+        if (K == 4) {
+#pragma unroll
+            for (int k = 0; k < 3; ++k) old_in[k] = old_quad(k, c_first);
+        }
+        if (tid < nx) scale_in = *reinterpret_cast<const float4*>(scales + tid * 4);
     }
     asm volatile("griddepcontrol.launch_dependents;\n" ::: "memory");
     if (tid < n_heads) {
@@ -253,80 +260,81 @@ __global__ void __launch_bounds__(kThreads, kMinBlocks) q8_update_kernel(const Q
     }
     __syncthreads();
 
-    // ---- conv: one word of channels at a time, x of the tile, then B and C
+    // ---- conv: four channels at a time, x of the tile, then B and C
     {
-        auto conv_word = [&](int q, uint32_t raw, uint32_t bias_w, uint4 wv) {
+        auto conv_quad = [&](int q, int c0, V4 raw, V4 bias_v, const Taps& taps, const V4 (&old)[3], float4 sc) {
             const bool is_x = q < nx;
-            const int j = is_x ? q * CW : (q - nx) * CW;  // channel within the segment(s)
-            const int seg = j >= N ? 1 : 0;               // (B, C) 0 or 1
-            const int64_t c0 = word_channel(q);
-            const AT* rows = is_x ? s_cx + j : s_cbc + seg * (K - 1) * N + (j - seg * N);
-            const int pitch = is_x ? a.tile_rows : N;
-            float out[CW];
-            unpack_word<AT>(bias_w, out);
-            if (K == 4) {  // the CW x 4 weights are one 16-byte vector
-                float w4[Vec16<AT>::n], xv[CW];
-                unpack16<AT>(wv, w4);
-                unpack_word<AT>(raw, xv);
+            const int j = is_x ? q * 4 : (q - nx) * 4;  // channel within x, or within (B, C)
+            const float4 b4 = Q::unpack(bias_v);
+            float2 out01 = make_float2(b4.x, b4.y), out23 = make_float2(b4.z, b4.w);
+            auto tap = [&](V4 row, const float (&wk)[4]) {
+                const float4 r = Q::unpack(row);
+                out01 = __ffma2_rn(make_float2(wk[0], wk[1]), make_float2(r.x, r.y), out01);
+                out23 = __ffma2_rn(make_float2(wk[2], wk[3]), make_float2(r.z, r.w), out23);
+            };
+            if (K == 4) {
+                float f[16];
 #pragma unroll
-                for (int k = 0; k < 3; ++k) {
-                    float rv[CW];
-                    unpack_word<AT>(*reinterpret_cast<const uint32_t*>(rows + k * pitch), rv);
+                for (int i = 0; i < AS; ++i) unpack16<AT>(taps.v[i], f + i * Vec16<AT>::n);
 #pragma unroll
-                    for (int e = 0; e < CW; ++e) out[e] = fmaf(w4[e * 4 + k], rv[e], out[e]);
+                for (int k = 0; k < 4; ++k) {
+                    const float wk[4] = {f[k], f[4 + k], f[8 + k], f[12 + k]};
+                    tap(k < 3 ? old[k] : raw, wk);
                 }
-#pragma unroll
-                for (int e = 0; e < CW; ++e) out[e] = fmaf(w4[e * 4 + 3], xv[e], out[e]);
             } else {
+                const AT* wc = w + static_cast<int64_t>(c0) * K;
                 for (int k = 0; k < K; ++k) {
-                    float rv[CW];
-                    unpack_word<AT>(k < K - 1 ? *reinterpret_cast<const uint32_t*>(rows + k * pitch) : raw, rv);
-#pragma unroll
-                    for (int e = 0; e < CW; ++e) out[e] = fmaf(to_f32(__ldg(w + (c0 + e) * K + k)), rv[e], out[e]);
+                    const float wk[4] = {to_f32(__ldg(wc + k)), to_f32(__ldg(wc + K + k)), to_f32(__ldg(wc + 2 * K + k)),
+                                         to_f32(__ldg(wc + 3 * K + k))};
+                    tap(k < K - 1 ? old_quad(k, c0) : raw, wk);
                 }
             }
             if (a.activation) {
-#pragma unroll
-                for (int e = 0; e < CW; ++e) out[e] = silu_f32(out[e]);
+                out01 = silu2_f32(out01);
+                out23 = silu2_f32(out23);
             }
-            if (is_x) {
-                for (int k = 0; k < K - 1; ++k)  // roll this CTA's own conv rows
-                    *reinterpret_cast<uint32_t*>(conv0 + k * cd + c0) =
-                        k < K - 2 ? *reinterpret_cast<const uint32_t*>(rows + (k + 1) * pitch) : raw;
-                const int hl = head_of(rr0 + j);  // CW channels lie in one head
-                const float dtv = s_dt[hl], dAv = s_dA[hl], Dv = s_D[hl];
-#pragma unroll
-                for (int e = 0; e < CW; ++e) {
-                    s_rp[j + e] = make_float2(dtv * out[e], s_scale[j + e] * dAv);
-                    s_y[j + e] = Dv * out[e];
+            // the rolled conv rows: this CTA's own into the cache, the group's aside for the end
+            auto roll_into = [&](V4* row, int64_t pitch) {
+                if (K == 4) {
+                    row[0] = old[1];
+                    row[pitch] = old[2];
+                    row[2 * pitch] = raw;
+                } else {
+                    for (int k = 0; k < K - 1; ++k) row[k * pitch] = k < K - 2 ? old_quad(k + 1, c0) : raw;
                 }
+            };
+            if (is_x) {
+                roll_into(reinterpret_cast<V4*>(conv0 + c0), cd / 4);
+                const int hl = head_of(rr0 + j);  // 4 channels lie in one head
+                const float2 dtv = make_float2(s_dt[hl], s_dt[hl]), Dv = make_float2(s_D[hl], s_D[hl]);
+                const float dAv = s_dA[hl];
+                const float2 u01 = __fmul2_rn(dtv, out01), u23 = __fmul2_rn(dtv, out23);
+                float4* rp = reinterpret_cast<float4*>(s_rp + j);
+                rp[0] = make_float4(u01.x, sc.x * dAv, u01.y, sc.y * dAv);
+                rp[1] = make_float4(u23.x, sc.z * dAv, u23.y, sc.w * dAv);
+                const float2 y01 = __fmul2_rn(Dv, out01), y23 = __fmul2_rn(Dv, out23);
+                *reinterpret_cast<float4*>(s_y + j) = make_float4(y01.x, y01.y, y23.x, y23.y);
             } else {
-                float* dst = (seg ? s_C : s_B) + bc_place<LPR>(j - seg * N);
-#pragma unroll
-                for (int e = 0; e < CW; ++e) dst[e] = out[e];
-                s_rawbc[j / CW] = raw;
+                float* dst = j < N ? s_B + bc_place<LPR>(j) : s_C + bc_place<LPR>(j - N);
+                *reinterpret_cast<float4*>(dst) = make_float4(out01.x, out01.y, out23.x, out23.y);
+                if (cluster_rank() == 0) roll_into(s_roll + j / 4, N / 2);
             }
         };
-        if (mbar_wait_bounded(bar_conv, 0, kWaitLimitNs)) {
+        if (q_first) conv_quad(tid, c_first, raw_in, bias_in, w_in, old_in, scale_in);
+        for (int q = kThreads + tid; q < n_quads; q += kThreads) {
+            const int c0 = quad_channel(q);
+            V4 old[3]{};
+            if (K == 4) {
 #pragma unroll
-            for (int i = 0; i < kPre; ++i) {
-                const int q = i * kThreads + tid;
-                if (q < n_words) conv_word(q, raw_in[i], bias_in[i], w_in[i]);
+                for (int k = 0; k < 3; ++k) old[k] = old_quad(k, c0);
             }
-            for (int q = kPre * kThreads + tid; q < n_words; q += kThreads) {
-                const int64_t c0 = word_channel(q);
-                conv_word(q, *reinterpret_cast<const uint32_t*>(xrow + c0),
-                          bias ? __ldg(reinterpret_cast<const uint32_t*>(bias + c0)) : 0u,
-                          K == 4 ? __ldg(reinterpret_cast<const uint4*>(w + c0 * 4)) : make_uint4(0, 0, 0, 0));
-            }
-        } else {
-            record_error(a.error, M2_ERR_TIMEOUT);
-            s_fail = 1;
+            conv_quad(q, c0, quad_of(xrow + c0), bias ? quad_of(bias + c0) : V4{}, K == 4 ? taps_of(c0) : Taps{}, old,
+                      q < nx ? *reinterpret_cast<const float4*>(scales + q * 4) : make_float4(0.f, 0.f, 0.f, 0.f));
         }
-        cluster_arrive_relaxed();  // this CTA has read the group's B/C conv rows
     }
     __syncthreads();
-    bool ok = s_fail == 0;
+    cluster_arrive_relaxed();  // this CTA has read the group's B/C conv rows
+    bool ok = true;
 
     // ---- the state, two rows a thread at a time
     const int lane = tid & 31;
@@ -407,30 +415,35 @@ __global__ void __launch_bounds__(kThreads, kMinBlocks) q8_update_kernel(const Q
     }
     if (!ok) {  // let this CTA's copies land before its shared memory goes
         for (int c = 0; c < copies; ++c) mbar_wait_bounded(&s_bar[c], 0, kWaitLimitNs);
-        mbar_wait_bounded(bar_conv, 0, kWaitLimitNs);
     }
     __syncthreads();
 
-    if (ok) {
-        for (int i = tid; i < nrows; i += kThreads) scales[i] = s_scale[i];
+    if (ok) {  // by the threads that have fewer rows of y
+        for (int i = kThreads - 1 - tid; i < nx; i += kThreads)
+            reinterpret_cast<float4*>(scales)[i] = reinterpret_cast<const float4*>(s_scale)[i];
     }
+    // four rows' gated y
+    auto gated = [&](int q) -> float4 {
+        float4 v = reinterpret_cast<const float4*>(s_y)[q];
+        if (zrow) {
+            const float4 z4 = Q::unpack(q == tid ? z_in : quad_of(zrow + r0 + q * 4));
+            const float2 g01 = silu2_f32(make_float2(z4.x, z4.y)), g23 = silu2_f32(make_float2(z4.z, z4.w));
+            v = make_float4(v.x * g01.x, v.y * g01.y, v.z * g23.x, v.w * g23.y);
+        }
+        return v;
+    };
     if constexpr (!NORM) {
         if (ok) {
-            for (int i = tid; i < nrows; i += kThreads) {
-                float yv = s_y[i];
-                if (zrow) yv *= silu_f32(to_f32(zrow[r0 + i]));
-                yrow[r0 + i] = from_f32<AT>(yv);
-            }
+            for (int q = tid; q < nx; q += kThreads) reinterpret_cast<V4*>(yrow + r0)[q] = Q::pack(gated(q));
         }
     } else {
         // gated RMSNorm over the group's rows, which are this cluster's
         float ss = 0.f;
         if (ok) {
-            for (int i = tid; i < nrows; i += kThreads) {
-                float yv = s_y[i];
-                if (zrow) yv *= silu_f32(to_f32(zrow[r0 + i]));
-                s_y[i] = yv;
-                ss = fmaf(yv, yv, ss);
+            for (int q = tid; q < nx; q += kThreads) {
+                const float4 v = gated(q);
+                reinterpret_cast<float4*>(s_y)[q] = v;
+                ss += (v.x * v.x + v.y * v.y) + (v.z * v.z + v.w * v.w);
             }
         }
 #pragma unroll
@@ -461,13 +474,9 @@ __global__ void __launch_bounds__(kThreads, kMinBlocks) q8_update_kernel(const Q
     // ---- cluster rank 0 rolls the group's B and C conv rows
     if (!NORM && cluster_rank() == 0) cluster_wait();
     if (ok && cluster_rank() == 0) {
-        for (int q = tid; q < 2 * N / CW; q += kThreads) {
-            const int j = q * CW, seg = j / N;
-            const int64_t c0 = (seg ? cC : cB) + (j - seg * N);
-            const AT* rows = s_cbc + seg * (K - 1) * N + (j - seg * N);
-            for (int k = 0; k < K - 1; ++k)
-                *reinterpret_cast<uint32_t*>(conv0 + k * cd + c0) =
-                    k < K - 2 ? *reinterpret_cast<const uint32_t*>(rows + (k + 1) * N) : s_rawbc[q];
+        for (int q = tid; q < N / 2; q += kThreads) {
+            V4* row = reinterpret_cast<V4*>(conv0 + quad_channel(nx + q));
+            for (int k = 0; k < K - 1; ++k) row[k * (cd / 4)] = s_roll[k * (N / 2) + q];
         }
     }
 }
