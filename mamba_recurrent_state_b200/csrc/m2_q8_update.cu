@@ -10,8 +10,11 @@
 //  * A sequence's state is H*P rows of N codes. The rows of an SSM group are
 //    cut into tiles of tile_rows rows (the last may be short), a CTA of 128
 //    threads each, the group's CTAs one thread-block cluster.
-//  * One thread puts the slot's conv rows, the tile's scales and the codes in
-//    flight as bulk copies before anything else is computed.
+//  * One thread puts the tile's codes in flight as one bulk copy as soon as the
+//    slot is known; the slot's conv rows and scales go to registers, four
+//    channels a thread, the parameters before them (with the conv rows as bulk
+//    copies too, one thread's nine more issues held up the codes: 35.9 us in
+//    place of 33.1 for 64 Nemotron-H rows).
 //  * LPR = N/16 lanes share a row, 16 codes (one 16-byte vector) a lane. A
 //    thread works on two rows at once: their S' stay in registers while the
 //    sums y and the maxima a go over the LPR lanes, both with the first level
@@ -26,10 +29,12 @@
 //    conv of its x channels and of the group's B and C; cluster rank 0 alone
 //    rolls the group's B/C conv rows, after all have read them.
 //
-// Bound by instruction issue beside HBM: a code takes 0.34 warp instructions, all
-// included (unpack, update, y, maximum, round, pack, exchanges, conv), which for
-// 64 Nemotron-H rows is 20 us of the SMs' issue slots beside 23 us of HBM time,
-// and a CTA's wait for its rows overlaps only with other CTAs' arithmetic.
+// Bound by instruction issue beside HBM: 32 codes take 10 warp instructions (5 a
+// lane's code for unpack, update, y, maximum, round and pack; a row's exchanges
+// and a tile's conv and output the rest), for 64 Nemotron-H rows 19 us of the
+// SMs' issue slots beside 23 us of HBM time, and a CTA's wait for its codes
+// overlaps only with other CTAs' arithmetic. 384 rows: 166.7 us, 0.83 of the copy
+// bandwidth; one row 3.9 us.
 #include <cuda_runtime.h>
 
 #include <algorithm>
@@ -40,12 +45,13 @@ namespace m2 {
 namespace {
 
 // Threads of a CTA, rows of its tile, the resident CTAs per SM that the
-// registers are sized for (five do reside: 90 registers, 43 KB), passes over the
+// registers are sized for (five do reside: 96 registers, 40 KB), passes over the
 // tile that one copy brings. 64 Nemotron-H rows (23.2 us at the copy bandwidth):
-// 128, 256, 4, 8 passes 35.8 us; sized for three CTAs 39.1 (126 registers, four
-// reside), for five 42.1 (the compiler trades registers for instructions); 192
-// rows 43.4; 256 threads 57.5, with 512 rows 52.3 us; two rings of 256 rows, the
-// next row's copies under this one's arithmetic, 54.3 us.
+// 128, 256, 4, 8 passes 32.0 us; sized for five CTAs 34.7 (fewer registers, more
+// instructions); four passes a copy 32.9; tiles of 128 rows 36.7, of 512 45.2;
+// 256 threads with 512 rows 38.1, 64 threads with 128 38.8 us. A persistent CTA
+// with two rings, the next row's copies under this one's arithmetic, took half
+// as long again.
 constexpr int kThreads = 128;
 constexpr int kTileRows = 256;
 constexpr int kMinBlocks = 4;
@@ -355,62 +361,64 @@ __global__ void __launch_bounds__(kThreads, kMinBlocks) q8_update_kernel(const Q
     const uint8_t* codes = s_codes + tid * 16;
     int8_t* out = tile + tid * 16;
     const int end = nrows * N - tid * 16;  // codes of this thread's rows that exist lie below
-#pragma unroll 1
-    for (int c = 0; c < passes; ++c) {
-        if (c % kCopyPasses == 0 && !mbar_wait_bounded(&s_bar[c / kCopyPasses], 0, kWaitLimitNs)) {
+    for (int first = 0; first < passes; first += kCopyPasses) {
+        if (!mbar_wait_bounded(&s_bar[first / kCopyPasses], 0, kWaitLimitNs)) {
             record_error(a.error, M2_ERR_TIMEOUT);
             ok = false;
             break;
         }
-        float2 S[kRowsPerThread][8];
-        float sum[kRowsPerThread], big[kRowsPerThread];
+#pragma unroll 1
+        for (int c = first; c < min(first + kCopyPasses, passes); ++c) {
+            float2 S[kRowsPerThread][8];
+            float sum[kRowsPerThread], big[kRowsPerThread];
 #pragma unroll
-        for (int i = 0; i < kRowsPerThread; ++i) {
-            const float2 rp = rps[(c * kRowsPerThread + i) * RPP];
-            const uint4 w = *reinterpret_cast<const uint4*>(codes + (c * kRowsPerThread + i) * (kThreads * 16));
-            const uint32_t words[4] = {w.x, w.y, w.z, w.w};
-            const float2 dtx = make_float2(rp.x, rp.x), k2 = make_float2(rp.y, rp.y);
-            float2 acc;
-            float m = 0.f;
+            for (int i = 0; i < kRowsPerThread; ++i) {
+                const float2 rp = rps[(c * kRowsPerThread + i) * RPP];
+                const uint4 w = *reinterpret_cast<const uint4*>(codes + (c * kRowsPerThread + i) * (kThreads * 16));
+                const uint32_t words[4] = {w.x, w.y, w.z, w.w};
+                const float2 dtx = make_float2(rp.x, rp.x), k2 = make_float2(rp.y, rp.y);
+                float2 acc;
+                float m = 0.f;
 #pragma unroll
-            for (int q = 0; q < 4; ++q) {
-                float2 lo, hi;
-                q8_unpack(words[q], lo, hi);
-                lo = __ffma2_rn(lo, k2, __fmul2_rn(dtx, B2[2 * q]));
-                hi = __ffma2_rn(hi, k2, __fmul2_rn(dtx, B2[2 * q + 1]));
-                acc = q == 0 ? __fmul2_rn(lo, C2[0]) : __ffma2_rn(lo, C2[2 * q], acc);
-                acc = __ffma2_rn(hi, C2[2 * q + 1], acc);
-                m = max_abs(m, lo.x, lo.y);
-                m = max_abs(m, hi.x, hi.y);
-                S[i][2 * q] = lo;
-                S[i][2 * q + 1] = hi;
+                for (int q = 0; q < 4; ++q) {
+                    float2 lo, hi;
+                    q8_unpack(words[q], lo, hi);
+                    lo = __ffma2_rn(lo, k2, __fmul2_rn(dtx, B2[2 * q]));
+                    hi = __ffma2_rn(hi, k2, __fmul2_rn(dtx, B2[2 * q + 1]));
+                    acc = q == 0 ? __fmul2_rn(lo, C2[0]) : __ffma2_rn(lo, C2[2 * q], acc);
+                    acc = __ffma2_rn(hi, C2[2 * q + 1], acc);
+                    m = max_abs(m, lo.x, lo.y);
+                    m = max_abs(m, hi.x, hi.y);
+                    S[i][2 * q] = lo;
+                    S[i][2 * q + 1] = hi;
+                }
+                sum[i] = acc.x + acc.y;
+                big[i] = m;
             }
-            sum[i] = acc.x + acc.y;
-            big[i] = m;
-        }
-        const float ysum = reduce_two<LPR>(sum[0], sum[1], upper, [](float u, float v) { return u + v; });
-        const float amax = reduce_two<LPR>(big[0], big[1], upper, [](float u, float v) { return max_nan(u, v); });
-        float scale, inv;
-        q8_scale_fast(amax, scale, inv);
-        if (l % (LPR / 2) == 0) {
-            const int row = (c * kRowsPerThread + (upper ? 1 : 0)) * RPP + tid / LPR;  // < tile_rows
-            s_y[row] += ysum;
-            s_scale[row] = scale;
-        }
-        float inv_of[kRowsPerThread];
-        inv_of[0] = __shfl_sync(0xffffffffu, inv, lane & ~(LPR / 2));
-        inv_of[1] = __shfl_sync(0xffffffffu, inv, lane | (LPR / 2));
-#pragma unroll
-        for (int i = 0; i < kRowsPerThread; ++i) {
-            const float2 iv = make_float2(inv_of[i], inv_of[i]), mg = make_float2(kQ8Magic, kQ8Magic);
-            uint32_t o[4];
-#pragma unroll
-            for (int q = 0; q < 4; ++q) {
-                const float2 lo = __ffma2_rn(S[i][2 * q], iv, mg), hi = __ffma2_rn(S[i][2 * q + 1], iv, mg);
-                o[q] = q8_pack(lo.x, lo.y, hi.x, hi.y);
+            const float ysum = reduce_two<LPR>(sum[0], sum[1], upper, [](float u, float v) { return u + v; });
+            const float amax = reduce_two<LPR>(big[0], big[1], upper, [](float u, float v) { return max_nan(u, v); });
+            float scale, inv;
+            q8_scale_fast(amax, scale, inv);
+            if (l % (LPR / 2) == 0) {
+                const int row = (c * kRowsPerThread + (upper ? 1 : 0)) * RPP + tid / LPR;  // < tile_rows
+                s_y[row] += ysum;
+                s_scale[row] = scale;
             }
-            const int at = (c * kRowsPerThread + i) * (kThreads * 16);
-            if (at < end) st_stream(out + at, make_uint4(o[0], o[1], o[2], o[3]));
+            float inv_of[kRowsPerThread];
+            inv_of[0] = __shfl_sync(0xffffffffu, inv, lane & ~(LPR / 2));
+            inv_of[1] = __shfl_sync(0xffffffffu, inv, lane | (LPR / 2));
+#pragma unroll
+            for (int i = 0; i < kRowsPerThread; ++i) {
+                const float2 iv = make_float2(inv_of[i], inv_of[i]), mg = make_float2(kQ8Magic, kQ8Magic);
+                uint32_t o[4];
+#pragma unroll
+                for (int q = 0; q < 4; ++q) {
+                    const float2 lo = __ffma2_rn(S[i][2 * q], iv, mg), hi = __ffma2_rn(S[i][2 * q + 1], iv, mg);
+                    o[q] = q8_pack(lo.x, lo.y, hi.x, hi.y);
+                }
+                const int at = (c * kRowsPerThread + i) * (kThreads * 16);
+                if (at < end) st_stream(out + at, make_uint4(o[0], o[1], o[2], o[3]));
+            }
         }
     }
     if (!ok) {  // let this CTA's copies land before its shared memory goes
@@ -546,10 +554,11 @@ cudaError_t launch_q8_update(Q8UpdateArgs a, cudaStream_t stream) {
     if (cudaGetDevice(&dev) != cudaSuccess || cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess)
         sms = 148;
     // few rows: halve the tiles as long as that brings idle SMs in and the
-    // cluster stays portable (one Nemotron-H row: 6.2 us with 256 rows a tile, 4.9
-    // with 128; five 7.2 and 6.2)
+    // cluster stays portable (Nemotron-H, 256 rows a tile and 128:
+    // one row 4.9 and 3.9 us, five 6.2 and 5.4, twelve 11.5 and 10.6, sixteen
+    // 12.5 and 12.9)
     while (tile % (2 * pass_rows(a.N)) == 0 && 2 * ((group_rows + tile - 1) / tile) <= 8 &&
-           static_cast<int64_t>(a.G) * ((group_rows + tile - 1) / tile) * a.batch < 2 * sms)
+           static_cast<int64_t>(a.G) * ((group_rows + tile - 1) / tile) * a.batch < 3 * sms)
         tile /= 2;
     a.group_rows = group_rows;
     a.hpg = a.H / a.G;
