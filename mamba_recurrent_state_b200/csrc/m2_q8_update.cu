@@ -29,9 +29,9 @@
 //    conv of its x channels and of the group's B and C; cluster rank 0 alone
 //    rolls the group's B/C conv rows, after all have read them.
 //
-// Bound by instruction issue beside HBM: 32 codes take 10 warp instructions (5 a
+// Bound by instruction issue beside HBM: 32 codes take 9.4 warp instructions (5 a
 // lane's code for unpack, update, y, maximum, round and pack; a row's exchanges
-// and a tile's conv and output the rest), for 64 Nemotron-H rows 19 us of the
+// and a tile's conv and output the rest), for 64 Nemotron-H rows 18 us of the
 // SMs' issue slots beside 23 us of HBM time, and a CTA's wait for its codes
 // overlaps only with other CTAs' arithmetic. 384 rows: 166.7 us, 0.83 of the copy
 // bandwidth; one row 3.9 us.
