@@ -88,6 +88,13 @@ struct Scan {
     // vectors are rotated (by multiples of four tokens), so that the helpers,
     // who write and read a token's channels, meet other banks.
     __device__ static __forceinline__ int place(int c, int t) { return (t + ROT * (c / VEC)) & (TT - 1); }
+    // The same for the states' rows of B and C: the helpers of a warp write
+    // BCV vectors of 32 / BCV tokens (1649 tokens of 4096 channels of 64 states:
+    // 248 us without, 188 us with). With fp32 activations, whose scan is bound by
+    // expf and where a vector holds fewer states than a channel has lanes, the
+    // places cost more than the conflicts (334 us without, 350 us with).
+    static constexpr int BC_ROT = Factors::kExact ? 0 : (32 / BCV > 4 ? 32 / BCV : 4);
+    __device__ static __forceinline__ int bc_place(int vec, int t) { return (t + BC_ROT * vec) & (TT - 1); }
     struct Buffer {
         float d[CB][P];     // dt
         float u[CB][P];     // dt * x
@@ -130,14 +137,18 @@ __device__ __forceinline__ void scan_tile(typename K::Buffer& buf, const float (
     const float* C = buf.bc[1][l];
     float* y = buf.y[lc];
     auto load4 = [](const float* p) { return *reinterpret_cast<const float4*>(p); };
+    // the vector that holds state s * LPC + l (a constant unless a vector is shorter than LPC)
+    const int lane_vec = K::BC_ROT != 0 && LPC > K::VEC ? l / K::VEC : 0;
+    auto at = [&](int s, int t) { return s * LPC * P + K::bc_place(s * LPC / K::VEC + lane_vec, t); };
     float4 d = load4(d_of + K::place(lc, 0)), u = load4(u_of + K::place(lc, 0)), b[SPL], c[SPL];
 #pragma unroll
     for (int s = 0; s < SPL; ++s) {
-        b[s] = load4(B + s * LPC * P);
-        if constexpr (Y) c[s] = load4(C + s * LPC * P);
+        b[s] = load4(B + at(s, 0));
+        if constexpr (Y) c[s] = load4(C + at(s, 0));
     }
     float2 last01 = make_float2(0.f, 0.f), last23 = last01;
-#pragma unroll kUnroll4
+    constexpr int kUnroll = TT <= 32 && !K::Factors::kExact ? TT / 4 : kUnroll4;
+#pragma unroll kUnroll
     for (int t = 0; t < TT; t += 4) {
         const float2 d01 = make_float2(d.x, d.y), d23 = make_float2(d.z, d.w), u01 = make_float2(u.x, u.y), u23 = make_float2(u.z, u.w);
         if constexpr (!Y) sum_dt += (d.x + d.y) + (d.z + d.w);
@@ -148,8 +159,8 @@ __device__ __forceinline__ void scan_tile(typename K::Buffer& buf, const float (
         u = load4(u_of + K::place(lc, tn));
 #pragma unroll
         for (int s = 0; s < SPL; ++s) {
-            nb[s] = load4(B + s * LPC * P + tn);
-            if constexpr (Y) nc[s] = load4(C + s * LPC * P + tn);
+            nb[s] = load4(B + at(s, tn));
+            if constexpr (Y) nc[s] = load4(C + at(s, tn));
         }
         float2 y01, y23;
 #pragma unroll
@@ -341,7 +352,7 @@ __global__ void __launch_bounds__(kThreads, kMinBlocks) sel_scan_kernel(const Se
                 float f[VEC];
                 unpack16<AT>(bcr[v], f);
 #pragma unroll
-                for (int e = 0; e < VEC; ++e) buf.bc[which][n + e][t] = f[e];
+                for (int e = 0; e < VEC; ++e) buf.bc[which][n + e][K::bc_place(n / VEC, t)] = f[e];
             }
         }
         bar_arrive(kFull + (q & 1));
