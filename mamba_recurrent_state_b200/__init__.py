@@ -644,10 +644,13 @@ def _param(t: Optional[torch.Tensor], name: str, n: int, dtype: torch.dtype, dev
         raise ValueError(f"{name} must be {n} contiguous {dtype} on {device}")
 
 
-def _current(device: torch.device) -> None:
-    """The library launches on the current device: the cache has to be there."""
-    if device.type != "cuda" or device.index != torch.cuda.current_device():
+def _stream_on(device: torch.device, stream: Optional[int] = None) -> int:
+    """The stream to launch on: ``stream``, or the current one. The library
+    launches on the current device: the cache has to be there. (The handle is
+    asked for directly: a torch.cuda.Stream object costs 3 us a call.)"""
+    if device.type != "cuda" or device.index != torch._C._cuda_getDevice():
         raise ValueError(f"the cache is on {device}, which is not the current CUDA device")
+    return torch._C._cuda_getCurrentRawStream(device.index) if stream is None else stream
 
 
 def _on(device: torch.device):
@@ -692,16 +695,16 @@ class Q8Cache:
         return self._c
 
     def zero_slots(self, slot_idx: torch.Tensor) -> None:
-        _current(self.device)
+        cs = _stream_on(self.device)
         _index(slot_idx, "slot_idx", slot_idx.numel(), self.device)
-        _check(lib().m2_q8_zero_slots(ctypes.byref(self._c), slot_idx.numel(), slot_idx.data_ptr(), _stream_ptr()),
+        _check(lib().m2_q8_zero_slots(ctypes.byref(self._c), slot_idx.numel(), slot_idx.data_ptr(), cs),
                "m2_q8_zero_slots")
 
     def device_error(self) -> int:
         """Reads and clears the device error word (synchronises the stream)."""
-        _current(self.device)
+        cs = _stream_on(self.device)
         code = _I32()
-        _check(lib().m2_q8_get_device_error(ctypes.byref(self._c), _stream_ptr(), ctypes.byref(code)),
+        _check(lib().m2_q8_get_device_error(ctypes.byref(self._c), cs, ctypes.byref(code)),
                "m2_q8_get_device_error")
         return code.value
 
@@ -714,9 +717,9 @@ def _q8_copy(name: str, src, dst, src_idx: torch.Tensor, dst_idx: torch.Tensor, 
     full = dst if q8 is src else src
     if (full.c.device != q8.device.index) if full.native else (full.ssm.device != q8.device):
         raise ValueError("the two caches are on different devices")
-    _current(q8.device)
-    _check(getattr(lib(), name)(ctypes.byref(src.c), ctypes.byref(dst.c), n, src_idx.data_ptr(), dst_idx.data_ptr(),
-                                _stream_ptr() if stream is None else stream), name)
+    cs = _stream_on(q8.device, stream)
+    _check(getattr(lib(), name)(ctypes.byref(src.c), ctypes.byref(dst.c), n, src_idx.data_ptr(), dst_idx.data_ptr(), cs),
+           name)
 
 
 def q8_store(src: Cache, dst: Q8Cache, src_idx: torch.Tensor, dst_idx: torch.Tensor,
@@ -747,7 +750,7 @@ def q8_state_update(cache: Q8Cache, ssm: SSMParams, conv: ConvParams, xBC: torch
     act = torch_dtype(sh.act_dtype)
     batch, hp = xBC.shape[0], sh.H * sh.P
     if y is None:
-        y = torch.empty((batch, hp), dtype=act, device=dev)
+        y = xBC.new_empty((batch, hp))
     cd = sh.conv_dim
     xs, ds = _rows(xBC, "xBC", batch, cd, act, dev), _rows(dt, "dt", batch, sh.H, act, dev)
     zs, ys = _rows(z, "z", batch, hp, act, dev), _rows(y, "y", batch, hp, act, dev)
@@ -759,11 +762,10 @@ def q8_state_update(cache: Q8Cache, ssm: SSMParams, conv: ConvParams, xBC: torch
     _param(conv.bias, "conv bias", cd, act, dev)
     if norm is not None:
         _param(norm.weight, "norm weight", hp, act, dev)
-    _current(dev)
+    cs = _stream_on(dev, stream)
     sp = m2_ssm_params(ssm.A_log.data_ptr(), ssm.dt_bias.data_ptr(), ssm.D.data_ptr())
     cp = m2_conv_params(conv.weight.data_ptr(), _ptr(conv.bias), conv.activation)
-    rest = (batch, xBC.data_ptr(), xs, dt.data_ptr(), ds, _ptr(z), zs, y.data_ptr(), ys, slot_idx.data_ptr(),
-            _stream_ptr() if stream is None else stream)
+    rest = (batch, xBC.data_ptr(), xs, dt.data_ptr(), ds, _ptr(z), zs, y.data_ptr(), ys, slot_idx.data_ptr(), cs)
     if norm is not None:
         npar = norm.c()
         _check(lib().m2_q8_state_update_norm(ctypes.byref(cache._c), ctypes.byref(sp), ctypes.byref(cp),
@@ -827,16 +829,16 @@ class SelCache:
         return self._c
 
     def zero_slots(self, slot_idx: torch.Tensor) -> None:
-        _current(self.device)
+        cs = _stream_on(self.device)
         _index(slot_idx, "slot_idx", slot_idx.numel(), self.device)
-        _check(lib().m2_sel_zero_slots(ctypes.byref(self._c), slot_idx.numel(), slot_idx.data_ptr(), _stream_ptr()),
+        _check(lib().m2_sel_zero_slots(ctypes.byref(self._c), slot_idx.numel(), slot_idx.data_ptr(), cs),
                "m2_sel_zero_slots")
 
     def device_error(self) -> int:
         """Reads and clears the device error word (synchronises the stream)."""
-        _current(self.device)
+        cs = _stream_on(self.device)
         code = _I32()
-        _check(lib().m2_sel_get_device_error(ctypes.byref(self._c), _stream_ptr(), ctypes.byref(code)),
+        _check(lib().m2_sel_get_device_error(ctypes.byref(self._c), cs, ctypes.byref(code)),
                "m2_sel_get_device_error")
         return code.value
 
@@ -886,13 +888,13 @@ def sel_state_update(cache: SelCache, params: SelParams, x: torch.Tensor, dt: to
     ``cache`` (m2_sel_state_update): x (post-conv), dt, z [batch, D], B and C
     [batch, G, N]. Returns y [batch, D]."""
     if y is None:
-        y = torch.empty((x.shape[0], cache.shape.D), dtype=torch_dtype(cache.shape.act_dtype), device=cache.device)
+        y = x.new_empty((x.shape[0], cache.shape.D))
     rows = _sel_rows(cache, x, dt, B, C, z, y)
     _index(slot_idx, "slot_idx", x.shape[0], cache.device)
     sp = params.c(cache.shape, cache.device)
-    _current(cache.device)
-    _check(lib().m2_sel_state_update(ctypes.byref(cache._c), ctypes.byref(sp), x.shape[0], *rows, slot_idx.data_ptr(),
-                                     _stream_ptr() if stream is None else stream), "m2_sel_state_update")
+    cs = _stream_on(cache.device, stream)
+    _check(lib().m2_sel_state_update(ctypes.byref(cache._c), ctypes.byref(sp), x.shape[0], *rows, slot_idx.data_ptr(), cs),
+           "m2_sel_state_update")
     return y
 
 
@@ -908,7 +910,7 @@ def sel_scan(cache: SelCache, params: SelParams, x: torch.Tensor, dt: torch.Tens
     nseq = cu_seqlens.numel() - 1
     _need(nseq >= 0, "cu_seqlens must hold nseq + 1 offsets")
     if y is None:
-        y = torch.empty((x.shape[0], cache.shape.D), dtype=torch_dtype(cache.shape.act_dtype), device=dev)
+        y = x.new_empty((x.shape[0], cache.shape.D))
     rows = _sel_rows(cache, x, dt, B, C, z, y)
     _index(cu_seqlens, "cu_seqlens", nseq + 1, dev)
     _index(slot_idx, "slot_idx", nseq, dev)
@@ -916,10 +918,10 @@ def sel_scan(cache: SelCache, params: SelParams, x: torch.Tensor, dt: torch.Tens
         _param(has_initial_state, "has_initial_state", nseq, has_initial_state.dtype, dev)
         _need(has_initial_state.dtype in (torch.uint8, torch.bool), "has_initial_state must be uint8 or bool")
     sp = params.c(cache.shape, dev)
-    _current(dev)
+    cs = _stream_on(dev, stream)
     _check(lib().m2_sel_scan(ctypes.byref(cache._c), ctypes.byref(sp), nseq, cu_seqlens.data_ptr(), x.shape[0],
                              x.shape[0] if max_seqlen is None else max_seqlen, *rows, slot_idx.data_ptr(),
-                             _ptr(has_initial_state), _stream_ptr() if stream is None else stream), "m2_sel_scan")
+                             _ptr(has_initial_state), cs), "m2_sel_scan")
     return y
 
 
@@ -928,7 +930,7 @@ def _sel_conv_args(cache: SelCache, conv: ConvParams, x: torch.Tensor, out: Opti
     sh, dev = cache.shape, cache.device
     act = torch_dtype(sh.act_dtype)
     if out is None:
-        out = torch.empty(x.shape, dtype=out_dtype or act, device=dev)
+        out = x.new_empty(x.shape, dtype=out_dtype or act)
     _param(conv.weight, "conv weight", sh.D * sh.K, act, dev)
     _param(conv.bias, "conv bias", sh.D, act, dev)
     return out, _rows(x, "x", x.shape[0], sh.D, act, dev), _rows(out, "out", x.shape[0], sh.D, out.dtype, dev)
@@ -942,10 +944,10 @@ def sel_conv1d_update(cache: SelCache, conv: ConvParams, x: torch.Tensor, slot_i
     out, xs, os_ = _sel_conv_args(cache, conv, x, out, out_dtype)
     _index(slot_idx, "slot_idx", x.shape[0], cache.device)
     cp = conv.c()
-    _current(cache.device)
+    cs = _stream_on(cache.device, stream)
     _check(lib().m2_sel_conv1d_update(ctypes.byref(cache.c), ctypes.byref(cp), x.shape[0], 1, x.data_ptr(), xs,
-                                      out.data_ptr(), _dtype_code(out.dtype), os_, slot_idx.data_ptr(),
-                                      _stream_ptr() if stream is None else stream), "m2_sel_conv1d_update")
+                                      out.data_ptr(), _dtype_code(out.dtype), os_, slot_idx.data_ptr(), cs),
+           "m2_sel_conv1d_update")
     return out
 
 
@@ -961,10 +963,10 @@ def sel_conv1d_update_varlen(cache: SelCache, conv: ConvParams, x: torch.Tensor,
     _index(cu_seqlens, "cu_seqlens", nseq + 1, cache.device)
     _index(slot_idx, "slot_idx", nseq, cache.device)
     cp = conv.c()
-    _current(cache.device)
+    cs = _stream_on(cache.device, stream)
     _check(lib().m2_sel_conv1d_update_varlen(ctypes.byref(cache.c), ctypes.byref(cp), nseq, cu_seqlens.data_ptr(),
                                              x.shape[0], x.shape[0] if max_seqlen is None else max_seqlen,
                                              x.data_ptr(), xs, out.data_ptr(), _dtype_code(out.dtype), os_,
-                                             slot_idx.data_ptr(), _stream_ptr() if stream is None else stream),
+                                             slot_idx.data_ptr(), cs),
            "m2_sel_conv1d_update_varlen")
     return out
