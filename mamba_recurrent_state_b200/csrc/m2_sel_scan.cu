@@ -38,7 +38,8 @@ constexpr int kThreads = kScan + kHelp;
 // Resident CTAs per SM that the registers are sized for (128 each; with three,
 // the scan of eight states a lane spills: 1870 us in place of 762 us for
 // 8 x 2048 tokens of 8192 channels), and blocks of four tokens that the scan
-// unrolls (two: 926 us).
+// unrolls (two: 926 us) where a tile is longer than 32 tokens or the decays call
+// expf; otherwise it unrolls the tile, so that places in it are constants.
 constexpr int kMinBlocks = 2;
 constexpr int kUnroll4 = 4;
 
@@ -215,7 +216,7 @@ __global__ void __launch_bounds__(kThreads, kMinBlocks) sel_scan_kernel(const Se
         if (threadIdx.x == 0 && blockIdx.x == 0 && g == 0) record_error(a.error, M2_ERR_BAD_SLOT);
         return;
     }
-    const int all_tiles = (T + TT - 1) / TT;
+    const int all_tiles = T / TT + (T % TT != 0);
     const int per_segment = segments > 1 ? (all_tiles + segments - 1) / segments : all_tiles;
     const int first = rank * per_segment, last = min(first + per_segment, all_tiles);  // this CTA's tiles
     const bool ahead = segments > 1 && last < all_tiles;  // a later segment needs this one's end
@@ -291,7 +292,8 @@ __global__ void __launch_bounds__(kThreads, kMinBlocks) sel_scan_kernel(const Se
     const AT* z = a.z ? static_cast<const AT*>(a.z) + row0 * a.z_stride + c0 + vc : nullptr;
     AT* y = static_cast<AT*>(a.y) + row0 * a.y_stride + c0 + vc;
     if (slot < 0) {  // padding: y = 0, the caches stay
-        for (int64_t t = first * TT + vt; t < min(last * TT, T) && vc_ok; t += VT)
+        const int64_t end = min(static_cast<int64_t>(last) * TT, static_cast<int64_t>(T));
+        for (int64_t t = static_cast<int64_t>(first) * TT + vt; t < end && vc_ok; t += VT)
             *reinterpret_cast<uint4*>(y + t * a.y_stride) = make_uint4(0, 0, 0, 0);
         return;
     }

@@ -445,6 +445,25 @@ def test_scans_on_two_streams_and_in_a_graph():
         assert all(torch.equal(u, v) for u, v in zip(got[i], want[i])) and torch.equal(first[i].ssm, second[i].ssm)
 
 
+@pytest.mark.gpu
+@pytest.mark.parametrize("channels,act,out", [(8, BF16, torch.float32), (12, F32, torch.bfloat16)], ids=["bf16", "f32"])
+def test_conv_of_few_channels(channels, act, out):
+    """A vector or three of channels, a long prompt and a short one; outputs of another type in a wider buffer."""
+    shape = m2.SelShape(channels, 16, 1, 4, F32, act)
+    layer, cache = Layer(shape, 72), cache_of(shape, 2)
+    before, buffer = cache.conv.clone(), torch.full((72, 16), 7.0, dtype=out, device="cuda")
+    got = m2.sel_conv1d_update_varlen(cache, layer.taps, layer.x, offsets([70, 2]), ints(1, 0), 70, out=buffer[:, :channels])
+    for slot, x, y in ((1, layer.x[:70], got[:70]), (0, layer.x[70:], got[70:])):
+        raw = torch.cat([before[slot], x])
+        pre = torch.einsum("tck,ck->tc", raw.double().unfold(0, 4, 1), layer.taps.weight.double()) + layer.taps.bias.double()
+        want = pre * torch.sigmoid(pre)
+        size = torch.einsum("tck,ck->tc", raw.double().abs().unfold(0, 4, 1), layer.taps.weight.double().abs()) + layer.taps.bias.double().abs()
+        # 1e-5 of the sum's size for its fp32 terms and the SiLU, half a step of the output type
+        assert ((y.double() - want).abs() <= 1e-5 * size + torch.finfo(out).eps / 2 * want.abs()).all()
+        assert torch.equal(cache.conv[slot], raw[-3:])
+    assert (buffer[:, channels:] == 7).all()
+
+
 # ---- the path as it is used ------------------------------------------------------
 
 @pytest.mark.gpu
