@@ -26,6 +26,7 @@
 #include <cuda_runtime.h>
 
 #include <algorithm>
+#include <cmath>
 
 #include "m2_sel.cuh"
 
@@ -440,36 +441,54 @@ cudaError_t launch_one(const SelArgs& a, int segments, cudaStream_t s) {
 
 // How the channels are spread: lanes a channel and segments a sequence. Fewer
 // states a lane make a token shorter and need more CTAs; segments run every
-// token twice. Measured time a token of a CTA in ns, by the states a lane has,
-// with one CTA an SM and with two (the 16384-token prompt of 2048 channels, the
-// 8 x 2048 tokens of 8192), and what a segment's two runs and the exchange
-// take over one run: 2.3 and 6 us. The plan is the cheapest by these.
+// token twice. Measured, ns a token of a CTA by the states that a lane has, for
+// 16- and 32-bit activations: with one CTA an SM, with two; and the two runs of a
+// segment's token with few clusters (up to half the SMs in CTAs) and with
+// many (two CTAs an SM; 33 clusters of 8 fit). A segment's exchange and second
+// start take 3 us. The plan is the cheapest by these; a batch counts as
+// many of its longest sequence as its tokens make, and shorter ones fill the
+// last round of CTAs. What that gives at 16384
+// tokens of 16 states: 512 channels 140 us (two states a lane in segments; 459 us
+// without), 1024 222 (four, segments; 390 with eight), 2048 425 (eight, segments),
+// 4096 578 (four; 676 with two), 8192 944 (four; 1060 with eight).
+constexpr int kSegments = 8;
 struct Plan {
     int lpc, segments;
 };
 Plan plan_scan(const SelArgs& a) {
     static const struct {
-        int states, one, two;  // ns
-    } kTimes[] = {{8, 67, 93}, {4, 45, 69}, {2, 29, 44}};
+        int states;
+        double one, two, few, many;
+    } kTimes[2][3] = {{{8, 62, 97, 118, 200}, {4, 36, 58, 65, 106}, {2, 29, 41, 46, 68}},
+                      {{8, 122, 188, 219, 355}, {4, 65, 105, 110, 187}, {2, 36, 56, 60, 97}}};
     int dev = 0, sms = 148;
     if (cudaGetDevice(&dev) != cudaSuccess || cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess)
         sms = 148;
-    const int64_t T = std::max<int64_t>(1, std::min<int64_t>(a.max_seqlen, a.total_tokens));
+    const double T = static_cast<double>(std::max<int64_t>(1, std::min<int64_t>(a.max_seqlen, a.total_tokens)));
+    const double seqs = std::min<double>(a.nseq, std::max(1., a.total_tokens / T));  // of the longest's length
     Plan best{};
     double best_ns = 0.;
-    for (const auto& k : kTimes) {
+    auto offer = [&](int lpc, int segments, double ns) {
+        if (best.lpc == 0 || ns < best_ns) {
+            best = {lpc, segments};
+            best_ns = ns;
+        }
+    };
+    for (auto k : kTimes[a.act_bf16 ? 0 : 1]) {
         const int lpc = a.N / k.states;
         if (lpc < 2 || lpc > 16) continue;
-        const int64_t ctas = static_cast<int64_t>(a.nseq) * a.G * ((a.D / a.G + kScan / lpc - 1) / (kScan / lpc));
-        for (int segments = 1; segments <= 8; segments *= 8) {
-            const int64_t n = ctas * segments;
-            const double ns = n <= sms ? k.one : static_cast<double>((n + 2 * sms - 1) / (2 * sms)) * k.two;
-            const double total = segments == 1 ? ns * T : ns * T / segments * 2.3 + 6000.;
-            if (best.lpc == 0 || total < best_ns) {
-                best = {lpc, segments};
-                best_ns = total;
-            }
+        if (lpc == 2) {  // 64 channels a CTA: no shorter than the helpers' work
+            k.one = std::max(k.one, 58.);
+            k.two = std::max(k.two, 72.);
+            k.few = std::max(k.few, 76.);
+            k.many = std::max(k.many, 129.);
         }
+        const double blocks = static_cast<double>(a.G) * ((a.D / a.G + kScan / lpc - 1) / (kScan / lpc));
+        const double all = blocks * a.nseq, full = blocks * seqs, in_segments = all * kSegments;
+        const double rounds = std::max(1., seqs < a.nseq ? full / (2 * sms) : std::ceil(full / (2 * sms)));
+        offer(lpc, 1, T * (all <= sms ? k.one : full <= sms ? (k.one + k.two) / 2 : rounds * k.two));
+        const double twice = in_segments <= sms / 2 ? k.few : std::ceil(in_segments / (2 * sms * 8 / 9)) * k.many;
+        offer(lpc, kSegments, 3000. + T / kSegments * twice);
     }
     return best;
 }

@@ -238,6 +238,19 @@ def test_scan_in_segments(shape):
 
 
 @pytest.mark.gpu
+@pytest.mark.parametrize("shape", [m2.SelShape(256, 16, 1, 4, F32, BF16), m2.SelShape(1024, 16, 1, 4, BF16, BF16), m2.SelShape(2048, 16, 1, 4, F32, BF16),
+                                   m2.SelShape(1024, 16, 1, 4, F32, F32), m2.SelShape(512, 32, 2, 4, F32, BF16), m2.SelShape(256, 64, 2, 4, F32, BF16),
+                                   m2.SelShape(256, 8, 1, 4, F32, BF16)], ids=str)
+def test_one_long_prompt(shape):
+    """1100 tokens alone: two, four and eight states a lane in segments."""
+    layer, cache = Layer(shape, 1100), cache_of(shape, 1)
+    before = cache.ssm.clone()
+    y = m2.sel_scan(cache, layer.params, layer.x, layer.dt, layer.B, layer.C, offsets([1100]), ints(0), z=layer.z,
+                    has_initial_state=torch.ones(1, dtype=torch.uint8, device="cuda"))
+    check_scan(layer, cache, [1100], ints(0), [1], y, before)
+
+
+@pytest.mark.gpu
 @pytest.mark.parametrize("D", [512, 4096])
 def test_scan_of_many_channels(D):
     """Enough channels for every way of spreading a channel's states over lanes."""
