@@ -445,9 +445,9 @@ cudaError_t launch_one(const SelArgs& a, int segments, cudaStream_t s) {
 // 16- and 32-bit activations: with one CTA an SM, with two; and the two runs of a
 // segment's token with few clusters (up to half the SMs in CTAs) and with
 // many (two CTAs an SM; 33 clusters of 8 fit). A segment's exchange and second
-// start take 3 us. The plan is the cheapest by these; a batch counts as
-// many of its longest sequence as its tokens make, and shorter ones fill the
-// last round of CTAs. What that gives at 16384
+// start take 1 us, a round of CTAs 3 us to start and one of clusters 5. The plan
+// is the cheapest by these; a batch counts as many of its longest sequence as its tokens
+// make, and shorter ones fill the last round of CTAs. What that gives at 16384
 // tokens of 16 states: 512 channels 140 us (two states a lane in segments; 459 us
 // without), 1024 222 (four, segments; 390 with eight), 2048 425 (eight, segments),
 // 4096 578 (four; 676 with two), 8192 944 (four; 1060 with eight).
@@ -485,10 +485,13 @@ Plan plan_scan(const SelArgs& a) {
         }
         const double blocks = static_cast<double>(a.G) * ((a.D / a.G + kScan / lpc - 1) / (kScan / lpc));
         const double all = blocks * a.nseq, full = blocks * seqs, in_segments = all * kSegments;
-        const double rounds = std::max(1., seqs < a.nseq ? full / (2 * sms) : std::ceil(full / (2 * sms)));
-        offer(lpc, 1, T * (all <= sms ? k.one : full <= sms ? (k.one + k.two) / 2 : rounds * k.two));
-        const double twice = in_segments <= sms / 2 ? k.few : std::ceil(in_segments / (2 * sms * 8 / 9)) * k.many;
-        offer(lpc, kSegments, 3000. + T / kSegments * twice);
+        const bool ragged = seqs < a.nseq;
+        auto rounds = [&](double ctas, double places) { return std::max(1., ragged ? ctas / places : std::ceil(ctas / places)); };
+        const double places = 2. * sms, in_clusters = places * 8 / 9;
+        const double shared = k.one + (k.two - k.one) * std::min(1., std::max(.5, full / places));
+        offer(lpc, 1, 3000. * std::max(1., all / places) + T * (all <= sms ? k.one : shared * rounds(full, places)));
+        const double twice = in_segments <= sms / 2 ? k.few : k.many * rounds(full * kSegments, in_clusters);
+        offer(lpc, kSegments, 1000. + 5000. * std::max(1., in_segments / in_clusters) + T / kSegments * twice);
     }
     return best;
 }
