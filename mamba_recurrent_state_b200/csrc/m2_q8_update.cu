@@ -44,16 +44,17 @@
 namespace m2 {
 namespace {
 
-// Threads of a CTA, rows of its tile, the resident CTAs per SM that the
+// Threads of a CTA, codes of its tile, the resident CTAs per SM that the
 // registers are sized for (five do reside: 96 registers, 40 KB), passes over the
 // tile that one copy brings. 64 Nemotron-H rows (23.2 us at the copy bandwidth):
-// 128, 256, 4, 8 passes 32.0 us; sized for five CTAs 34.7 (fewer registers, more
+// 128, 256 rows, 4, 8 passes 32.0 us; sized for five CTAs 34.7 (fewer registers, more
 // instructions); four passes a copy 32.9; tiles of 128 rows 36.7, of 512 45.2;
 // 256 threads with 512 rows 38.1, 64 threads with 128 38.8 us. A persistent CTA
 // with two rings, the next row's copies under this one's arithmetic, took half
-// as long again.
+// as long again. Rows of 64 codes: 512 a tile 70.0 us for 256 rows of 128 heads,
+// 256 74.6; of 256 codes: 128 a tile 240 us, 256 255 us.
 constexpr int kThreads = 128;
-constexpr int kTileRows = 256;
+constexpr int kTileCodes = 32768;
 constexpr int kMinBlocks = 4;
 constexpr int kWarps = kThreads / 32;
 constexpr int kRowsPerThread = 2;
@@ -547,19 +548,24 @@ m2_status q8_shape_supported(int H, int P, int N, int G) {
 
 cudaError_t launch_q8_update(Q8UpdateArgs a, cudaStream_t stream) {
     const int group_rows = a.H / a.G * a.P;
-    int tile = std::min(kTileRows, max_tile(a.N));
+    int tile = std::min(kTileCodes / a.N, max_tile(a.N));
     if (group_rows < tile) tile = (group_rows + pass_rows(a.N) - 1) / pass_rows(a.N) * pass_rows(a.N);
     while ((group_rows + tile - 1) / tile > kMaxCluster) tile *= 2;
     int dev = 0, sms = 148;
     if (cudaGetDevice(&dev) != cudaSuccess || cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess)
         sms = 148;
-    // few rows: halve the tiles as long as that brings idle SMs in and the
-    // cluster stays portable (Nemotron-H, 256 rows a tile and 128:
-    // one row 4.9 and 3.9 us, five 6.2 and 5.4, twelve 11.5 and 10.6, sixteen
-    // 12.5 and 12.9)
-    while (tile % (2 * pass_rows(a.N)) == 0 && 2 * ((group_rows + tile - 1) / tile) <= 8 &&
-           static_cast<int64_t>(a.G) * ((group_rows + tile - 1) / tile) * a.batch < 3 * sms)
+    // few rows: halve the tiles as long as that brings idle SMs in, to clusters of
+    // 8 up to three CTAs an SM (Nemotron-H, 256 rows a tile and 128: one row 4.9
+    // and 3.9 us, five 6.2 and 5.4, twelve 11.5 and 10.6, sixteen 12.5 and 12.9),
+    // to clusters of 16 up to one (64 heads of 64 x 64 in one group, clusters
+    // of 8 and 16: one row 6.2 and 4.2 us, sixteen 7.0 and 5.6; 128 heads in eight
+    // groups, where 8 make 256 CTAs: four rows 4.2 and 4.9)
+    for (;;) {
+        const int ctas = (group_rows + tile - 1) / tile;
+        const int64_t all = static_cast<int64_t>(a.G) * ctas * a.batch;
+        if (tile % (2 * pass_rows(a.N)) != 0 || 2 * ctas > kMaxCluster || all >= (2 * ctas <= 8 ? 3 : 1) * sms) break;
         tile /= 2;
+    }
     a.group_rows = group_rows;
     a.hpg = a.H / a.G;
     a.inv_P = ((1u << 22) + a.P - 1) / a.P;
