@@ -491,7 +491,8 @@ typedef struct m2_q8_cache {
 } m2_q8_cache;
 
 /* M2_OK when the 8-bit kernels implement `shape` (N 64, 128 or 256, P a
- * multiple of 8 up to 256, and at most 8192 rows a group, 4096 at N = 256);
+ * multiple of 8 up to 256, at most 8192 rows a group, 4096 at N = 256, and
+ * at most 65535 groups);
  * otherwise as m2_shape_check. Host only, no CUDA. */
 m2_status m2_q8_shape_check(const m2_shape* shape);
 
@@ -567,9 +568,9 @@ m2_status m2_q8_get_device_error(const m2_q8_cache* cache, m2_stream stream, int
  * conv's output by the caller, so the conv is a call of its own.
  */
 typedef struct m2_sel_shape {
-    int32_t channels;    /* D */
+    int32_t channels;    /* D, at most 2^24 */
     int32_t d_state;     /* N: 8, 16, 32, 64 or 128 */
-    int32_t ngroups;     /* G, divides D; D/G channels must fill 16-byte vectors */
+    int32_t ngroups;     /* G <= 65535, divides D; D/G channels must fill 16-byte vectors */
     int32_t d_conv;      /* K, conv width (2..8) */
     int32_t state_dtype; /* M2_F32 or M2_BF16 */
     int32_t act_dtype;   /* of x, dt_raw, B, C, z, y and the conv (M2_F32 or M2_BF16) */
