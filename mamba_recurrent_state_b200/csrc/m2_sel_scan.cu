@@ -269,18 +269,21 @@ __global__ void __launch_bounds__(kThreads, kMinBlocks) sel_scan_kernel(const Se
                 for (int s = 0; s < SPL; ++s)
                     h[s] = fmaf(h[s], K::Factors::over(dt * A[s]), ld_cluster_f32(&sm.end_h[lc][s * LPC + l], r));
             }
-            cluster_arrive();  // done with the others' shared memory
+            cluster_arrive();  // done with the others' shared memory and with the slot's initial state
         }
         for (int i = first; i < last; ++i, ++q) {
             bar_sync(kFull + (q & 1));
             scan_tile<true, SPL, LPC, K>(sm.buf[q & 1], A, h, sum_dt, lc, l, tid & 31);
             bar_arrive(kDone + (q & 1));
         }
+        // The arrive above releases this CTA's reads of the others' shared memory and
+        // of the slot: after the wait the last segment may write the slot, and
+        // every CTA may leave.
+        if (segments > 1) cluster_wait();
         if (live && first < last && last == all_tiles) {
 #pragma unroll
             for (int s = 0; s < SPL; ++s) state[s * LPC] = from_f32<ST>(h[s]);
         }
-        if (segments > 1) cluster_wait();
         return;
     }
 

@@ -558,3 +558,33 @@ def test_a_prompt_in_two_parts_is_the_whole():
     size = layer.reference(cache_of(shape, 1).ssm[0], range(100))
     within(torch.cat(got), want.double(), size[2], 100, F32, "y")
     within(parts.ssm[0], whole.ssm[0].double(), size[3], 100, F32, "state")
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("shape,T,n", [(m2.SelShape(64, 16, 1, 4, F32, BF16), 256, 16), (m2.SelShape(16, 16, 1, 4, F32, BF16), 512, 16),
+                                       (m2.SelShape(64, 16, 1, 4, F32, F32), 250, 16), (m2.SelShape(16, 128, 2, 4, BF16, BF16), 128, 8),
+                                       (m2.SelShape(16, 64, 1, 4, F32, F32), 1000, 8)], ids=str)
+def test_segments_start_from_the_initial_state(shape, T, n):
+    """Every segment of a sequence reads the slot's state at the start of the
+    call, though the last one leaves the new state there: with a tile or two a
+    segment, over and over on the same inputs, the same bits, and those of the
+    recurrence. (States of 50 in size: a segment that began from the final state
+    would be far off.)"""
+    layer, cache = Layer(shape, n * T, seed=11), cache_of(shape, n, seed=12)
+    cache.ssm.mul_(500)
+    before = cache.ssm.clone()
+    slots = torch.randperm(n, generator=torch.Generator().manual_seed(1)).to(torch.int32).cuda()
+    one = torch.ones(n, dtype=torch.uint8, device="cuda")
+    first = None
+    for _ in range(40):
+        cache.ssm.copy_(before)
+        y = m2.sel_scan(cache, layer.params, layer.x, layer.dt, layer.B, layer.C, offsets([T] * n), slots, max_seqlen=T, z=layer.z,
+                        has_initial_state=one)
+        if first is None:
+            first = (y, cache.ssm.clone())
+        assert torch.equal(y, first[0]) and torch.equal(cache.ssm, first[1])
+    for i in (0, n - 1):
+        s, rows = int(slots[i]), range(i * T, (i + 1) * T)
+        ref, h, ysize, hsize = layer.reference(before[s], rows)
+        within(y[i * T:(i + 1) * T], ref, ysize, T, shape.act_dtype, f"y of sequence {i}")
+        within(cache.ssm[s], h, hsize, T, shape.state_dtype, f"state of sequence {i}")
