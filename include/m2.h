@@ -605,7 +605,8 @@ m2_status m2_sel_cache_wrap(const m2_sel_shape* shape, int64_t num_slots, void* 
 m2_status m2_sel_zero_slots(const m2_sel_cache* cache, int32_t n, const int32_t* slot_idx, m2_stream stream);
 
 /* m2_conv1d_update and m2_conv1d_update_varlen over the D channels of x:
- * weight [D, K], bias [D] or NULL. */
+ * weight [D, K], bias [D] or NULL. At most 2^31 - 2^24 tokens a call
+ * (M2_ERR_UNSUPPORTED otherwise). */
 m2_status m2_sel_conv1d_update(const m2_sel_cache* cache, const m2_conv_params* conv, int32_t batch,
                                int32_t seqlen, const void* x, int64_t x_row_stride, void* x_out,
                                int32_t out_dtype, int64_t out_row_stride, const int32_t* slot_idx,
@@ -643,7 +644,8 @@ m2_status m2_sel_state_update(const m2_sel_cache* cache, const m2_sel_params* pa
  * fp32 activations every softplus and decay is the library's expf and log1pf;
  * with bf16 ones they come within 5e-7 from the special-function unit, and
  * silu(z) within 2^-10 of itself (for z < -6 within 2^-15): half a bf16 step is
- * 2^-9. At most 65535 sequences. One launch, no scratch memory.
+ * 2^-9. At most 65535 sequences and 2^31 - 2^24 tokens (M2_ERR_UNSUPPORTED
+ * otherwise). One launch, no scratch memory.
  */
 m2_status m2_sel_scan(const m2_sel_cache* cache, const m2_sel_params* params, int32_t nseq,
                       const int32_t* cu_seqlens, int64_t total_tokens, int32_t max_seqlen, const void* x,

@@ -12,6 +12,11 @@ using namespace m2::host;
 
 namespace {
 
+// The kernels number a sequence's tokens in 32 bits and step past the last one:
+// the conv by up to three strides of its grid, 3 * 65535 * 32 tokens, the scan by
+// a tile. Calls stay below 2^31 by more than that.
+constexpr int64_t kMaxTokens = (int64_t{1} << 31) - (int64_t{1} << 24);
+
 m2_status sel_shape_status(const m2_sel_shape* s) {
     if (!s) return M2_ERR_INVALID_ARG;
     if (s->channels <= 0 || s->d_state <= 0 || s->ngroups <= 0 || s->d_conv <= 0) return M2_ERR_INVALID_ARG;
@@ -183,7 +188,7 @@ m2_status m2_sel_zero_slots(const m2_sel_cache* c, int32_t n, const int32_t* slo
 m2_status m2_sel_conv1d_update(const m2_sel_cache* c, const m2_conv_params* conv, int32_t batch, int32_t seqlen,
                                const void* x, int64_t x_row_stride, void* x_out, int32_t out_dtype,
                                int64_t out_row_stride, const int32_t* slot_idx, m2_stream stream) {
-    if (batch > 0 && seqlen > 0 && static_cast<int64_t>(batch) * seqlen > INT32_MAX) return M2_ERR_UNSUPPORTED;
+    if (batch > 0 && seqlen > 0 && static_cast<int64_t>(batch) * seqlen > kMaxTokens) return M2_ERR_UNSUPPORTED;
     return conv_impl(c, conv, batch, seqlen, nullptr, static_cast<int64_t>(batch) * seqlen, x, x_row_stride, x_out,
                      out_dtype, out_row_stride, slot_idx, stream);
 }
@@ -193,7 +198,7 @@ m2_status m2_sel_conv1d_update_varlen(const m2_sel_cache* c, const m2_conv_param
                                       const void* x, int64_t x_row_stride, void* x_out, int32_t out_dtype,
                                       int64_t out_row_stride, const int32_t* slot_idx, m2_stream stream) {
     if (nseq < 0 || total_tokens < 0 || max_seqlen < 0) return M2_ERR_INVALID_ARG;
-    if (total_tokens > INT32_MAX) return M2_ERR_UNSUPPORTED;
+    if (total_tokens > kMaxTokens) return M2_ERR_UNSUPPORTED;
     if (nseq > 0 && total_tokens > 0 && !cu_seqlens) return M2_ERR_INVALID_ARG;
     const int32_t len = (nseq == 0 || total_tokens == 0) ? 0 : std::max(max_seqlen, 1);
     return conv_impl(c, conv, nseq, len, cu_seqlens, total_tokens, x, x_row_stride, x_out, out_dtype, out_row_stride,
@@ -224,7 +229,7 @@ m2_status m2_sel_scan(const m2_sel_cache* c, const m2_sel_params* p, int32_t nse
     m2_status st = sel_status(c);
     if (st != M2_OK) return st;
     if (!params_ok(p) || nseq < 0 || total_tokens < 0 || max_seqlen < 0) return M2_ERR_INVALID_ARG;
-    if (total_tokens > INT32_MAX) return M2_ERR_UNSUPPORTED;
+    if (total_tokens > kMaxTokens) return M2_ERR_UNSUPPORTED;
     if (nseq == 0 || total_tokens == 0) return M2_OK;
     if (!cu_seqlens) return M2_ERR_INVALID_ARG;
     m2::SelArgs a{};

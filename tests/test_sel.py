@@ -588,3 +588,30 @@ def test_segments_start_from_the_initial_state(shape, T, n):
         ref, h, ysize, hsize = layer.reference(before[s], rows)
         within(y[i * T:(i + 1) * T], ref, ysize, T, shape.act_dtype, f"y of sequence {i}")
         within(cache.ssm[s], h, hsize, T, shape.state_dtype, f"state of sequence {i}")
+
+
+def test_too_many_tokens_are_refused_on_the_host():
+    """A kernel's token numbers have 32 bits and run past the last token by what its
+    CTAs have in flight: a call takes 2^31 - 2^24 tokens at most."""
+    L = m2.lib()
+    s = m2.SelShape(8, 8, 1, 4, F32, BF16).c()
+    cache = m2.m2_sel_cache()
+    assert L.m2_sel_cache_wrap(ctypes.byref(s), 4, 0x100000, 0x200000, None, ctypes.byref(cache)) == m2.M2_OK
+    p, taps, buf = m2.m2_sel_params(0x300000, 0x300100, 0x300200), m2.m2_conv_params(0x500000, None, 1), 0x400000
+
+    def scan(total):  # (x is missing: no call gets past the checks)
+        return L.m2_sel_scan(ctypes.byref(cache), ctypes.byref(p), 1, buf, total, 5, None, 8, buf, 8, buf, 8, buf, 8, None, 0, buf, 8, buf, None, None)
+
+    def conv(total):
+        return L.m2_sel_conv1d_update_varlen(ctypes.byref(cache), ctypes.byref(taps), 1, buf, total, 5, None, 8, buf, BF16, 8, buf, None)
+
+    def conv_rows(batch, seqlen):
+        return L.m2_sel_conv1d_update(ctypes.byref(cache), ctypes.byref(taps), batch, seqlen, None, 8, buf, BF16, 8, buf, None)
+
+    most = 2**31 - 2**24
+    for call in (scan, conv):
+        for total in (most + 1, 2**31 - 100, 2**31 - 1, 2**31):
+            assert call(total) == m2.M2_ERR_UNSUPPORTED, (call, total)
+        assert call(most) == m2.M2_ERR_INVALID_ARG  # not refused for its size, but for what is missing
+    assert conv_rows(1, most + 1) == m2.M2_ERR_UNSUPPORTED and conv_rows(2**15, 2**16 - 1) == m2.M2_ERR_UNSUPPORTED
+    assert conv_rows(1, most) == m2.M2_ERR_INVALID_ARG
