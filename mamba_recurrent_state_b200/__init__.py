@@ -320,8 +320,9 @@ class Cache:
         assert ssm.is_contiguous() and conv.is_contiguous()
         self.ssm, self.conv = ssm, conv
         self.error = torch.zeros(1, dtype=torch.int32, device=ssm.device)
-        _check(lib().m2_cache_wrap(ctypes.byref(s), num_slots, ssm.data_ptr(), conv.data_ptr(),
-                                   self.error.data_ptr(), ctypes.byref(self._c)), "m2_cache_wrap")
+        with _on(ssm.device):
+            _check(lib().m2_cache_wrap(ctypes.byref(s), num_slots, ssm.data_ptr(), conv.data_ptr(),
+                                       self.error.data_ptr(), ctypes.byref(self._c)), "m2_cache_wrap")
 
     @property
     def c(self) -> m2_cache:

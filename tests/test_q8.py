@@ -517,3 +517,13 @@ def test_prefill_park_decode_resume_verify():
     rel = lambda u, v: float((u.float() - v.float()).norm() / v.float().norm())  # noqa: E731
     assert rel(ya, yb) <= limit and rel(ys[0], ys[1]) <= limit
     assert q8.device_error() == 0 and full.device_error() == 0
+
+
+def test_a_cache_is_described_on_the_device_of_its_tensors(monkeypatch):
+    """Whatever device is current when the handle is made."""
+    seen = []
+    on = m2._on
+    monkeypatch.setattr(m2, "_on", lambda device: (seen.append(device), on(device))[1])
+    shape = m2.Shape(8, 64, 128, 1, 4)
+    cache = m2.Cache(shape, 2, device="cpu")
+    assert seen == [cache.ssm.device]
