@@ -521,7 +521,8 @@ m2_status m2_q8_zero_slots(const m2_q8_cache* cache, int32_t n, const int32_t* s
  * a negative index is skipped; an index past its cache's slots records
  * M2_ERR_BAD_SLOT in that cache's error word and skips the pair. src_idx may
  * repeat a slot; the non-negative dst_idx must be distinct (M2_VALIDATE=1
- * checks). Both caches are on the current device. One launch.
+ * checks). Both caches are on the current device (M2_ERR_INVALID_ARG
+ * otherwise). One launch.
  */
 m2_status m2_q8_store(const m2_cache* src, const m2_q8_cache* dst, int32_t n, const int32_t* src_idx,
                       const int32_t* dst_idx, m2_stream stream);

@@ -44,7 +44,7 @@ m2_status copy_impl(const m2_cache* full, const m2_q8_cache* q8, bool store, int
         return M2_ERR_INVALID_ARG;
     if (n < 0 || (n > 0 && (!src_idx || !dst_idx))) return M2_ERR_INVALID_ARG;
     if (n == 0) return M2_OK;
-    if (!on_current_device(q8->device)) return M2_ERR_INVALID_ARG;
+    if (!on_current_device(q8->device) || !on_current_device(full->device)) return M2_ERR_INVALID_ARG;
     const cudaStream_t cs = reinterpret_cast<cudaStream_t>(stream);
     if (validate_mode()) {
         const m2_status v = validate_slots(dst_idx, n, store ? q8->num_slots : full->num_slots, cs);

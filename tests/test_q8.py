@@ -527,3 +527,21 @@ def test_a_cache_is_described_on_the_device_of_its_tensors(monkeypatch):
     shape = m2.Shape(8, 64, 128, 1, 4)
     cache = m2.Cache(shape, 2, device="cpu")
     assert seen == [cache.ssm.device]
+
+
+@pytest.mark.gpu
+def test_copies_refuse_a_cache_of_another_device():
+    """Either of the two caches described on a device that is not the current one:
+    refused on the host, by the library itself."""
+    shape = m2.Shape(8, 64, 128, 1, 4, BF16, BF16)
+    full, q8 = caches(shape, 2, 2)
+    i = torch.zeros(1, dtype=torch.int32, device="cuda")
+    L, here = m2.lib(), full.c.device
+    for handle in (full.c, q8.c):
+        handle.device = here + 1
+        rest = (1, i.data_ptr(), i.data_ptr(), torch.cuda.current_stream().cuda_stream)
+        assert L.m2_q8_store(ctypes.byref(full.c), ctypes.byref(q8.c), *rest) == m2.M2_ERR_INVALID_ARG
+        assert L.m2_q8_load(ctypes.byref(q8.c), ctypes.byref(full.c), *rest) == m2.M2_ERR_INVALID_ARG
+        handle.device = here
+    m2.q8_store(full, q8, i, i)
+    assert torch.equal(q8.ssm[0], reference_codes(full.ssm[0].float())[0])
