@@ -474,7 +474,8 @@ m2_status m2_host_stage_join(m2_host_stage* stage, m2_stream stream);
  *   a = max |v| over the row, both quotients rounded to fp32, then
  *   scale = a / 127,  code = round half to even (v * (127 / a)),
  * and a value reads back as code * scale, at most scale / 2 (and fp32
- * rounding) from v. (The decode step forms the quotients within 2^-22.) A row
+ * rounding) from v. (The decode step forms the quotients within 2^-22; where 127
+ * times the scale would pass the largest float, it is one float lower.) A row
  * with a < 2^-100 is stored as zeros, scale and codes. A row that holds an
  * infinity or a NaN reads back as NaN in every value: its scale is NaN.
  * Every store rounds: a state that stays parked is rounded once, one that

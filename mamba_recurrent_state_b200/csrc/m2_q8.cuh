@@ -5,6 +5,7 @@
 //   a < 2^-100        scale = 0, codes 0 (127 / a would overflow)
 //   a inf or NaN      scale = NaN: the whole row reads back as NaN
 //   else              scale = a / 127, code = round_half_even(v * (127 / a))
+//                     (the scale one float lower where 127 of it would pass the largest float)
 // both quotients rounded to fp32, the product not rounded before the code.
 // A value reads back as code * scale, at most scale / 2 from v (1 + 2^-22).
 //
@@ -85,13 +86,17 @@ __device__ __forceinline__ float max_nan(float a, float b) {
     return r;
 }
 
+// The largest scale: the float below the largest finite one over 127, whose
+// product with 127 would round to an infinity.
+constexpr float kQ8TopScale = 0x1.020406p+121f;
+
 // Scale and inverse of a row whose largest magnitude is a.
 __device__ __forceinline__ void q8_scale(float a, float& scale, float& inv) {
     const bool finite = a <= 3.402823466e38f;   // false for inf and NaN
     const bool live = finite && a >= 7.888609052e-31f;  // 2^-100
     const float d = live ? a : 1.f;
     inv = live ? __fdiv_rn(127.f, d) : 0.f;
-    scale = live ? __fdiv_rn(d, 127.f) : (finite ? 0.f : __int_as_float(0x7fc00000));
+    scale = live ? fminf(__fdiv_rn(d, 127.f), kQ8TopScale) : (finite ? 0.f : __int_as_float(0x7fc00000));
 }
 
 // The largest of m and the magnitudes of a and b; a NaN stays.

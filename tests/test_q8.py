@@ -545,3 +545,32 @@ def test_copies_refuse_a_cache_of_another_device():
         handle.device = here
     m2.q8_store(full, q8, i, i)
     assert torch.equal(q8.ssm[0], reference_codes(full.ssm[0].float())[0])
+
+
+@pytest.mark.gpu
+def test_the_largest_finite_values_read_back_finite():
+    """127 times the rounded quotient of the largest float and 127 would be an infinity."""
+    shape = m2.Shape(8, 64, 128, 1, 4, F32, F32)
+    full, q8 = caches(shape, 2, 2)
+    top = torch.finfo(torch.float32).max
+    full.ssm[0, 0, 0, :4] = torch.tensor([top, -top, top / 2, 0.0])
+    full.ssm[0, 0, 1, 5] = -top
+    full.ssm[0, 0, 2, 0] = top * (1 - 2.0 ** -23)
+    i = torch.zeros(1, dtype=torch.int32, device="cuda")
+    want = full.ssm[0].clone()
+    m2.q8_store(full, q8, i, i)
+    m2.q8_load(q8, full, i, i)
+    assert torch.isfinite(full.ssm[0]).all()
+    # half a step, and the roundings to fp32 of scale, inverse and product
+    step = q8.scale[0].double()[..., None]
+    assert ((full.ssm[0].double() - want.double()).abs() <= step * (0.5 + 127 * 4 * 2.0 ** -24)).all()
+    # and through a decode step that keeps the state: dt of zero, no input
+    layer = Layer(shape, 1, z=False, bias=False)
+    layer.xBC.zero_()
+    layer.dt.fill_(-200)
+    q8.conv.zero_()
+    layer.run(q8, i)
+    m2.q8_load(q8, full, i, i)
+    assert torch.isfinite(full.ssm[0]).all()
+    step = q8.scale[0].double()[..., None]
+    assert ((full.ssm[0].double() - want.double()).abs() <= step * (0.5 + 127 * 6 * 2.0 ** -22)).all()
