@@ -645,8 +645,7 @@ m2_status m2_sel_state_update(const m2_sel_cache* cache, const m2_sel_params* pa
  * channel, so results of calls of other sizes can differ by fp32 rounding. With
  * fp32 activations every softplus and decay is the library's expf and log1pf;
  * with bf16 ones they come within 5e-7 from the special-function unit, and
- * silu(z) within 2^-10 of itself (for z < -6 within 2^-15): half a bf16 step is
- * 2^-9. At most 65535 sequences and 2^31 - 2^24 tokens (M2_ERR_UNSUPPORTED
+ * silu(z) within 1e-6 + |z| 2^-23 of itself. At most 65535 sequences and 2^31 - 2^24 tokens (M2_ERR_UNSUPPORTED
  * otherwise). One launch, no scratch memory.
  */
 m2_status m2_sel_scan(const m2_sel_cache* cache, const m2_sel_params* params, int32_t nseq,

@@ -86,6 +86,26 @@ __device__ __forceinline__ float2 softplus2_fast(float2 v) {
     return __ffma2_rn(p, u, make_float2(fmaxf(v.x, 0.f), fmaxf(v.y, 0.f)));
 }
 
+// silu of a pair with one special-function operation a value, within 1e-6 + |z| 2^-23
+// of itself (the rounding of the exponent): with u = exp(-|z|) in (0, 1] it is
+// z / (1 + u), below zero z u / (1 + u). The reciprocal of d = 1 + u starts from
+// (98 - 80 u + 32 u^2) / 99, the quadratic for which 1 - d r is the Chebyshev
+// polynomial T3(2 u - 1) over 99, and takes two Newton steps r += r (1 - d r), each of
+// which squares that error: 99^-4 = 1.0e-8. (8 x 2048 tokens of 8192 channels: 769 us;
+// with the unit's reciprocal, silu2_f32, 780; 740 with the hardware tanh, which is
+// off by 2^-12 of z, more than all of the value below z = -9.)
+__device__ __forceinline__ float2 silu2_newton(float2 z) {
+    const float2 u = make_float2(ex2_approx(-fabsf(z.x) * kLog2E), ex2_approx(-fabsf(z.y) * kLog2E));
+    auto both = [](float c) { return make_float2(c, c); };
+    const float2 minus_d = __ffma2_rn(u, both(-1.f), both(-1.f));
+    float2 r = __ffma2_rn(u, both(32.f / 99.f), both(-80.f / 99.f));
+    r = __ffma2_rn(r, u, both(98.f / 99.f));
+#pragma unroll
+    for (int i = 0; i < 2; ++i) r = __ffma2_rn(r, __ffma2_rn(minus_d, r, both(1.f)), r);
+    const float2 zu = __fmul2_rn(z, u);
+    return __fmul2_rn(make_float2(z.x < 0.f ? zu.x : z.x, z.y < 0.f ? zu.y : z.y), r);
+}
+
 template <typename AT>
 __device__ __forceinline__ float2 Decay<AT>::softplus(float2 v) {
     return kExact ? make_float2(softplus_f32(v.x), softplus_f32(v.y)) : softplus2_fast(v);

@@ -1,7 +1,7 @@
 // m2_sel_scan.cu -- the per-channel selective scan over packed prompts.
 //
-// Bound by the special-function unit: N + 2 exponentials and tanhs a (token,
-// channel), at 16 a cycle and SM, against 8 bytes of HBM traffic.
+// Bound by the special-function unit: N + 2 exponentials a (token, channel), at 16 a
+// cycle and SM, against 8 bytes of HBM traffic.
 //
 // A channel is handled by LPC lanes of a warp, SPL states a lane in registers.
 // A CTA has CB = 128 / LPC channels of one sequence and walks its tokens in
@@ -9,8 +9,7 @@
 //  * the helpers (128 threads) bring the inputs a tile ahead: they take 16-byte
 //    vectors of (token, channels) of x and dt, form dt = softplus(..) and dt * x,
 //    and leave both in shared memory, B and C beside them as floats; and they
-//    finish the tile that the scan has done: D x is added, y gated and stored
-//    (16-bit outputs with the tanh form of the SiLU, as the prefill conv);
+//    finish the tile that the scan has done: D x is added, y gated and stored;
 //  * the scan (128 threads) runs h = h * exp(dt A) + (dt x) B and sums
 //    h * C, four tokens at a time: shared memory holds every channel's (and
 //    every state's) tokens side by side, so that a lane reads four tokens at
@@ -379,7 +378,7 @@ __global__ void __launch_bounds__(kThreads, kMinBlocks) sel_scan_kernel(const Se
                 float2 o = __ffma2_rn(skip, make_float2(xv[e], xv[e + 1]), make_float2(buf.y[vc + e][at], buf.y[vc + e + 1][at]));
                 if (z) {
                     const float2 zz = make_float2(zv[e], zv[e + 1]);
-                    o = __fmul2_rn(o, sizeof(AT) == 2 ? silu2_tanh_f32(zz) : silu2_f32(zz));
+                    o = __fmul2_rn(o, K::Factors::kExact ? silu2_f32(zz) : silu2_newton(zz));
                 }
                 out[e] = o.x;
                 out[e + 1] = o.y;

@@ -615,3 +615,62 @@ def test_too_many_tokens_are_refused_on_the_host():
         assert call(most) == m2.M2_ERR_INVALID_ARG  # not refused for its size, but for what is missing
     assert conv_rows(1, most + 1) == m2.M2_ERR_UNSUPPORTED and conv_rows(2**15, 2**16 - 1) == m2.M2_ERR_UNSUPPORTED
     assert conv_rows(1, most) == m2.M2_ERR_INVALID_ARG
+
+
+def bf16_values(low, high):
+    """Every bf16 value between low and high that is no denormal."""
+    v = torch.arange(-2**15, 2**15).to(torch.int16).view(torch.bfloat16).float()
+    v = v[torch.isfinite(v) & (v >= low) & (v <= high) & ((v.abs() >= 2.0 ** -20) | (v == 0))]
+    return v.unique().cuda()
+
+
+def grid_rows(values, D):
+    """The values as rows of D, the last one filled up."""
+    return torch.cat([values, values[-1:].expand(-len(values) % D)]).view(-1, D)
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("act", [BF16, F32], ids=["bf16", "f32"])
+def test_the_gate_from_far_below_to_far_above(act):
+    """y = x silu(z) for every bf16 z of -80 .. 80 (C = 0, D = 1), rounded once, of a
+    prompt and of tokens. The SiLU has an exponential, a sum, a reciprocal and a
+    product or two; -z log2(e) is rounded by 2^-24 of up to 116, which is 80 * 2^-24 of
+    the exponential, and its constant by 1.4e-8: 80 * 1.3 * 2^-24 + 4 * 2^-22 = 7.2e-6
+    in all."""
+    D = 64
+    shape = m2.SelShape(D, 16, 1, 4, F32, act)
+    z = grid_rows(bf16_values(-80.0, 80.0), D).to(TYPES[act])
+    T = z.shape[0]
+    layer = Layer(shape, T)
+    layer.C.zero_()
+    layer.params.D.fill_(1)
+    layer.x.copy_(torch.where(torch.arange(T, device="cuda")[:, None] % 2 == 0, 1.0, -3.0))
+    layer.z = z
+    gate = z.double() * torch.sigmoid(z.double())
+    want = layer.x.double() * gate
+    bound = (7.2e-6 + torch.finfo(TYPES[act]).eps / 2) * want.abs()
+    cache = cache_of(shape, T)
+    y = m2.sel_scan(cache, layer.params, layer.x, layer.dt, layer.B, layer.C, offsets([T]), ints(0), z=z)
+    off = ((y.double() - want).abs() / bound.clamp_min(1e-300)).max()
+    assert off <= 1, f"prompt: {off:.3g} times the bound"
+    slots = torch.arange(T, dtype=torch.int32, device="cuda")
+    tokens = m2.sel_state_update(cache, layer.params, layer.x, layer.dt, layer.B, layer.C, slots, z=z)
+    off = ((tokens.double() - want).abs() / bound.clamp_min(1e-300)).max()
+    assert off <= 1, f"tokens: {off:.3g} times the bound"
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("act", [BF16, F32], ids=["bf16", "f32"])
+def test_infinite_gates_stay_alone(act):
+    """silu(inf) = inf and a NaN stays one, each in its own value of y; states are untouched by z."""
+    shape = m2.SelShape(32, 16, 1, 4, F32, act)
+    layer = Layer(shape, 6)
+    plain, cache = cache_of(shape, 6), cache_of(shape, 6)
+    want = m2.sel_scan(plain, layer.params, layer.x, layer.dt, layer.B, layer.C, offsets([6]), ints(0), z=layer.z)
+    layer.z[2, 3], layer.z[4, 8] = float("inf"), float("nan")
+    y = m2.sel_scan(cache, layer.params, layer.x, layer.dt, layer.B, layer.C, offsets([6]), ints(0), z=layer.z)
+    tokens = m2.sel_state_update(cache_of(shape, 6), layer.params, layer.x, layer.dt, layer.B, layer.C, ints(0, 1, 2, 3, 4, 5), z=layer.z)
+    rest = torch.isfinite(layer.z)
+    for got in (y, tokens):
+        assert torch.isinf(got[2, 3]) and torch.isnan(got[4, 8]) and torch.isfinite(got[rest]).all()
+    assert torch.equal(y[rest], want[rest]) and torch.equal(plain.ssm, cache.ssm)
