@@ -644,8 +644,10 @@ m2_status m2_sel_state_update(const m2_sel_cache* cache, const m2_sel_params* pa
  * the decay of their summed dt, and a sum over N goes over the lanes of a
  * channel, so results of calls of other sizes can differ by fp32 rounding. With
  * fp32 activations every softplus and decay is the library's expf and log1pf;
- * with bf16 ones they come within 5e-7 from the special-function unit, and
- * silu(z) within 1e-6 + |z| 2^-23 of itself. At most 65535 sequences and 2^31 - 2^24 tokens (M2_ERR_UNSUPPORTED
+ * with bf16 ones they come from the special-function unit: dt = softplus(v)
+ * within 5e-7 + |v| 2^-23 of itself, a decay exp(dt A) within 3e-7 +
+ * |dt A| (1e-6 + (|v| + |A_log|) 2^-23). silu(z) is within 1e-6 + |z| 2^-23 of
+ * itself. At most 65535 sequences and 2^31 - 2^24 tokens (M2_ERR_UNSUPPORTED
  * otherwise). One launch, no scratch memory.
  */
 m2_status m2_sel_scan(const m2_sel_cache* cache, const m2_sel_params* params, int32_t nseq,

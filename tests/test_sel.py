@@ -674,3 +674,75 @@ def test_infinite_gates_stay_alone(act):
     for got in (y, tokens):
         assert torch.isinf(got[2, 3]) and torch.isnan(got[4, 8]) and torch.isfinite(got[rest]).all()
     assert torch.equal(y[rest], want[rest]) and torch.equal(plain.ssm, cache.ssm)
+
+
+def one_token_states(act, v, A_log, x, h0):
+    """The fp32 states after one token of each row of v (dt_raw, its bias zero; B = 1), by sel_scan and by sel_state_update."""
+    n, D = v.shape
+    shape = m2.SelShape(D, 16, 1, 4, F32, act)
+    dtype = TYPES[act]
+    params = m2.SelParams(A_log.contiguous(), torch.zeros(D, device="cuda"), torch.zeros(D, device="cuda"))
+    xs = torch.full((n, D), x, dtype=dtype, device="cuda")
+    B = torch.ones(n, 1, 16, dtype=dtype, device="cuda")
+    slots = torch.arange(n, dtype=torch.int32, device="cuda")
+    got = []
+    for scan in (True, False):
+        cache = m2.SelCache(shape, n)
+        cache.ssm.fill_(h0)
+        if scan:
+            m2.sel_scan(cache, params, xs, v.to(dtype), B, B, offsets([1] * n), slots, max_seqlen=1,
+                        has_initial_state=torch.ones(n, dtype=torch.uint8, device="cuda"))
+        else:
+            m2.sel_state_update(cache, params, xs, v.to(dtype), B, B, slots)
+        got.append(cache.ssm.double())
+    return got
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("act", [BF16, F32], ids=["bf16", "f32"])
+def test_softplus_within_its_bound(act):
+    """A state that one token starts from zero with x = B = 1 is dt itself, in fp32:
+    within 5e-7 + |v| 2^-23 of softplus(v) for every bf16 v of -86 .. 80."""
+    v = grid_rows(bf16_values(-86.0, 80.0), 64)
+    want = torch.nn.functional.softplus(v.double(), threshold=60).clamp_min(0)
+    want = torch.where(v < -30, v.double().exp(), want)[..., None]
+    bound = (5e-7 + v.double().abs() * 2.0 ** -23)[..., None] * want
+    for name, got in zip(("scan", "token"), one_token_states(act, v, torch.zeros(64, 16, device="cuda"), 1.0, 0.0)):
+        off = ((got - want).abs() / bound).max()
+        assert off <= 1, f"{name}: {off:.3g} times the bound"
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("act", [BF16, F32], ids=["bf16", "f32"])
+def test_decays_within_their_bound(act):
+    """A state of one that a token of x = 0 leaves is the decay exp(dt A): within
+    3e-7 + |dt A| (1e-6 + (|v| + |A_log|) 2^-23) of itself."""
+    v = grid_rows(bf16_values(-12.0, 6.0), 64)
+    A_log = torch.linspace(-6, 4, 64 * 16, device="cuda").view(64, 16)
+    dtA = torch.nn.functional.softplus(v.double(), threshold=40)[..., None] * A_log.double().exp()
+    want = torch.exp(-dtA)
+    bound = (3e-7 + dtA * (1e-6 + (v.double().abs()[..., None] + A_log.double().abs()) * 2.0 ** -23)) * want + 2.0 ** -125
+    for name, got in zip(("scan", "token"), one_token_states(act, v, A_log, 0.0, 1.0)):
+        off = ((got - want).abs() / bound).max()
+        assert off <= 1, f"{name}: {off:.3g} times the bound"
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("dt", [60.0, 19.0, -12.0, -120.0])
+@pytest.mark.parametrize("T", [12, 700], ids=["one run", "segments"])
+def test_scan_of_16_bit_inputs_at_the_ends_of_softplus(dt, T):
+    """As test_scan_at_the_ends_of_softplus, on the special-function unit's exponentials."""
+    shape = m2.SelShape(32, 16, 1, 4, F32, BF16)
+    layer = Layer(shape, T, z=False)
+    layer.dt.fill_(dt)
+    layer.params.dt_bias.zero_()
+    cache = cache_of(shape, 1)
+    before = cache.ssm.clone()
+    y = m2.sel_scan(cache, layer.params, layer.x, layer.dt, layer.B, layer.C, offsets([T]), ints(0),
+                    has_initial_state=torch.ones(1, dtype=torch.uint8, device="cuda"))
+    check_scan(layer, cache, [T], ints(0), [1], y, before)
+    one = cache_of(shape, 1)
+    first = m2.sel_state_update(one, layer.params, layer.x[:1], layer.dt[:1], layer.B[:1], layer.C[:1], ints(0))
+    ref, h, ysize, hsize = layer.reference(before[0], [0])
+    within(first, ref, ysize, 1, BF16, "y of the token")
+    within(one.ssm[0], h, hsize, 1, F32, "state of the token")
