@@ -746,3 +746,24 @@ def test_scan_of_16_bit_inputs_at_the_ends_of_softplus(dt, T):
     ref, h, ysize, hsize = layer.reference(before[0], [0])
     within(first, ref, ysize, 1, BF16, "y of the token")
     within(one.ssm[0], h, hsize, 1, F32, "state of the token")
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("act", [BF16, F32], ids=["bf16", "f32"])
+@pytest.mark.parametrize("T", [13, 777], ids=["one run", "segments"])
+def test_states_that_forget_everything(act, T):
+    """A_log of 100 and of +inf: such a state keeps its last token's addend alone,
+    also where tokens past the sequence's end (dt = 0) share its last tile."""
+    shape = m2.SelShape(24, 16, 1, 4, F32, act)
+    layer = Layer(shape, T)
+    layer.params.A_log[3, 5], layer.params.A_log[7, :8], layer.params.A_log[20] = float("inf"), 100.0, float("inf")
+    cache = cache_of(shape, 3)
+    before = cache.ssm.clone()
+    y = m2.sel_scan(cache, layer.params, layer.x, layer.dt, layer.B, layer.C, offsets([T]), ints(1), z=layer.z,
+                    has_initial_state=torch.ones(1, dtype=torch.uint8, device="cuda"))
+    check_scan(layer, cache, [T], ints(1), [1], y, before)
+    assert torch.isfinite(cache.ssm).all() and torch.isfinite(y).all()
+    token = m2.sel_state_update(cache, layer.params, layer.x[:1], layer.dt[:1], layer.B[:1], layer.C[:1], ints(2), z=layer.z[:1])
+    ref, h, ysize, hsize = layer.reference(before[2], [0])
+    within(token, ref, ysize, 1, act, "y of the token")
+    within(cache.ssm[2], h, hsize, 1, F32, "state of the token")
