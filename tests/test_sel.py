@@ -767,3 +767,18 @@ def test_states_that_forget_everything(act, T):
     ref, h, ysize, hsize = layer.reference(before[2], [0])
     within(token, ref, ysize, 1, act, "y of the token")
     within(cache.ssm[2], h, hsize, 1, F32, "state of the token")
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("batch", [1, 2, 9, 40])
+@pytest.mark.parametrize("state", [BF16, F32], ids=["bf16", "f32"])
+def test_tokens_row_by_row(batch, state):
+    """Every row of a batch with padding rows in it, and every slot beside them."""
+    shape = m2.SelShape(1040, 16, 2, 4, state, BF16)
+    layer, cache = Layer(shape, batch), cache_of(shape, 50)
+    slots = torch.randperm(50, device="cuda")[:batch].to(torch.int32)
+    slots[1::4] = -1
+    before = cache.ssm.clone()
+    y = m2.sel_state_update(cache, layer.params, layer.x, layer.dt, layer.B, layer.C, slots, z=layer.z)
+    check_scan(layer, cache, [1] * batch, slots, [1] * batch, y, before)
+    assert cache.device_error() == 0
