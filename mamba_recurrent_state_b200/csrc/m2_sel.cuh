@@ -50,7 +50,7 @@ constexpr float kLog2E = 1.4426950408889634f;
 
 // How exact the factors are goes by the activations' type. fp32 ones get the
 // library's expf and log1pf on dt * A itself, within an ulp or two each; for
-// 16-bit ones, whose own rounding is 2^-9, the special-function unit's 2^x
+// 16-bit ones, whose own rounding is 2^-8, the special-function unit's 2^x
 // (2^-22) of dt * (A log2 e) and the softplus below do: a decay is within 3e-7 +
 // |dt A| (1e-6 + (|v| + |A_log|) 2^-23) of itself, v = dt_raw + dt_bias.
 template <typename AT>
@@ -72,7 +72,7 @@ struct Decay {
 // 1.6e-7 with its fp32 roundings). One special-function operation a value; expf and
 // log1pf of the library take more, and a reciprocal for a series in u / (2 + u) one
 // more. Within 5e-7 + |v| 2^-23 of the value: the second part is the rounding of
-// -|v| log2 e, at v = -64 4e-6, where dt itself is 2e-28 (a bf16 v is known to |v| 2^-9).
+// -|v| log2 e, at v = -64 4e-6, where dt itself is 2e-28 (a bf16 v is known to |v| 2^-8).
 // Below v = -87 it is 0.
 __device__ __forceinline__ float2 softplus2_fast(float2 v) {
     const float2 u = make_float2(ex2_approx(-fabsf(v.x) * kLog2E), ex2_approx(-fabsf(v.y) * kLog2E));
