@@ -607,7 +607,9 @@ m2_status m2_sel_cache_wrap(const m2_sel_shape* shape, int64_t num_slots, void* 
 m2_status m2_sel_zero_slots(const m2_sel_cache* cache, int32_t n, const int32_t* slot_idx, m2_stream stream);
 
 /* m2_conv1d_update and m2_conv1d_update_varlen over the D channels of x:
- * weight [D, K], bias [D] or NULL. At most 2^31 - 2^24 tokens a call
+ * weight [D, K], bias [D] or NULL. Of bf16 prompts (32 tokens or more by the bound
+ * on their length) a 16-bit output takes the SiLU of v within 2^-12 of |v|, other
+ * outputs within fp32 rounding. At most 2^31 - 2^24 tokens a call
  * (M2_ERR_UNSUPPORTED otherwise). */
 m2_status m2_sel_conv1d_update(const m2_sel_cache* cache, const m2_conv_params* conv, int32_t batch,
                                int32_t seqlen, const void* x, int64_t x_row_stride, void* x_out,

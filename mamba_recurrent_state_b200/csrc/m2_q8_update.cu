@@ -33,8 +33,11 @@
 // codes (5 for unpack, update, y, maximum, round and pack; a row's exchanges and
 // a tile's conv and output the rest), for 64 Nemotron-H rows 18 us of the
 // SMs' issue slots beside 23 us of HBM time, and a CTA's wait for its codes
-// overlaps only with other CTAs' arithmetic. 384 rows: 166 us, 0.83 of the copy
-// bandwidth; one row 3.6 us.
+// overlaps only with other CTAs' arithmetic. 64 rows 32.1 us (floor 23.2), 384 rows
+// 165 us, 0.84 of the copy bandwidth; one row 3.4 us. With the norm 38.0 and 209 us:
+// two more cluster phases, and a CTA's tile waits for its group's. fp32 activations
+// 37.7 us for 64 rows (floor 25.0). K != 4 takes its taps one by one: K = 3 37.0 us
+// (22.8), K = 8 53.8 us (24.8).
 #include <cuda_runtime.h>
 
 #include <algorithm>

@@ -35,8 +35,9 @@ namespace {
 constexpr int kScan = 128;      // threads that run the recurrence
 constexpr int kHelp = 128;      // threads that bring the inputs and finish y
 constexpr int kThreads = kScan + kHelp;
-// Resident CTAs per SM that the registers are sized for (128 each; with three,
-// the scan of eight states a lane spills: 1870 us in place of 762 us for
+// Resident CTAs per SM that the registers are sized for (128 each, where eight states
+// a lane spill 8 to 40 bytes a thread with 16-bit activations and four states up to 20
+// with 32-bit ones; with three CTAs eight states took 1870 us in place of 762 us for
 // 8 x 2048 tokens of 8192 channels), and blocks of four tokens that the scan
 // unrolls (two: 926 us) where a tile is longer than 32 tokens or the decays call
 // expf; otherwise it unrolls the tile, so that places in it are constants.
@@ -91,7 +92,7 @@ struct Scan {
     __device__ static __forceinline__ int place(int c, int t) { return (t + ROT * (c / VEC)) & (TT - 1); }
     // The same for the states' rows of B and C: the helpers of a warp write
     // BCV vectors of 32 / BCV tokens (1649 tokens of 4096 channels of 64 states:
-    // 248 us without, 188 us with). With fp32 activations, whose scan is bound by
+    // 248 us without, 182 to 188 us with). With fp32 activations, whose scan is bound by
     // expf and where a vector holds fewer states than a channel has lanes, the
     // places cost more than the conflicts (334 us without, 350 us with).
     static constexpr int BC_ROT = Factors::kExact ? 0 : (32 / BCV > 4 ? 32 / BCV : 4);
@@ -450,9 +451,13 @@ cudaError_t launch_one(const SelArgs& a, int segments, cudaStream_t s) {
 // start take 1 us, a round of CTAs 3 us to start and one of clusters 5. The plan
 // is the cheapest by these; a batch counts as many of its longest sequence as its tokens
 // make, and shorter ones fill the last round of CTAs. What that gives at 16384
-// tokens of 16 states: 512 channels 140 us (two states a lane in segments; 459 us
-// without), 1024 222 (four, segments; 390 with eight), 2048 425 (eight, segments),
-// 4096 578 (four; 676 with two), 8192 944 (four; 1060 with eight).
+// tokens of 16 states: 512 channels 143 us (two states a lane in segments), 1024 228
+// (four, segments), 2048 438 (eight, segments), 4096 600 (four), 8192 982 (four). The
+// table and the other choices were timed with a gate of the hardware tanh, 2 to 4%
+// faster throughout: 512 channels 140 us, 459 without segments; 1024 222, 390 with
+// eight states a lane; 4096 578, 676 with two; 8192 944, 1060 with eight. Over 60 drawn
+// shapes the plan took 1.04 times the best one's time in the geometric mean, 1.43 times
+// at worst: prompts of a few tokens, where what a CTA takes to start decides.
 constexpr int kSegments = 8;
 struct Plan {
     int lpc, segments;

@@ -11,6 +11,12 @@
 // 16 bytes of a channel's states a lane, LPC = N * sizeof(state) / 16 lanes a
 // channel, and store the new state straight from registers. y goes over the
 // LPC lanes with xor shuffles. Waits are bounded as in m2_state_update.cu.
+//
+// 256 rows of 8192 channels of 16 states: fp32 states 50.1 us (0.88 of the copy
+// bandwidth), bf16 ones 38.7 us (floor 23.5): the same arithmetic on half the bytes,
+// bound by instruction issue (eight states a lane, 28 to 52 bytes of spill at 56
+// registers). With fp32 activations, whose decays call expf, 60.1 us (46.9) and 47.7
+// us (26.1).
 #include <cuda_runtime.h>
 
 #include <algorithm>
