@@ -649,8 +649,9 @@ m2_status m2_sel_state_update(const m2_sel_cache* cache, const m2_sel_params* pa
  * with bf16 ones they come from the special-function unit: dt = softplus(v)
  * within 5e-7 + |v| 2^-23 of itself, a decay exp(dt A) within 3e-7 +
  * |dt A| (1e-6 + (|v| + |A_log|) 2^-23). silu(z) is within 1e-6 + |z| 2^-23 of
- * itself. At most 65535 sequences and 2^31 - 2^24 tokens (M2_ERR_UNSUPPORTED
- * otherwise). One launch, no scratch memory.
+ * itself. (dt below v = -87 and silu below z = -87 are 0.) At most 65535 sequences
+ * and 2^31 - 2^24 tokens (M2_ERR_UNSUPPORTED otherwise). One launch, no scratch
+ * memory.
  */
 m2_status m2_sel_scan(const m2_sel_cache* cache, const m2_sel_params* params, int32_t nseq,
                       const int32_t* cu_seqlens, int64_t total_tokens, int32_t max_seqlen, const void* x,

@@ -89,7 +89,7 @@ __device__ __forceinline__ float2 softplus2_fast(float2 v) {
 }
 
 // silu of a pair with one special-function operation a value, within 1e-6 + |z| 2^-23
-// of itself (the rounding of the exponent): with u = exp(-|z|) in (0, 1] it is
+// of itself (the rounding of the exponent; 0 below z = -87): with u = exp(-|z|) in (0, 1] it is
 // z / (1 + u), below zero z u / (1 + u). The reciprocal of d = 1 + u starts from
 // (98 - 80 u + 32 u^2) / 99, the quadratic for which 1 - d r is the Chebyshev
 // polynomial T3(2 u - 1) over 99, and takes two Newton steps r += r (1 - d r), each of
